@@ -96,6 +96,7 @@ typedef enum {
 #define PA_DEVERR_BAD_BLOCK 0x1u   /* a table entry outside [0, num_blocks) */
 #define PA_DEVERR_BAD_LEN 0x2u     /* a sequence length beyond its table */
 #define PA_DEVERR_TIMEOUT 0x4u     /* a bounded wait on a copy gave up */
+#define PA_DEVERR_NO_BLOCKS 0x8u   /* pa_build_tables: more blocks needed than free ids given */
 
 typedef struct {
   int32_t num_layers;
@@ -265,6 +266,85 @@ pa_status pa_decode_attention_noalloc(const pa_pool_desc *desc, int32_t layer, i
  * Returns PA_ERR_DEVICE_CHECK if any bit was set, PA_ERR_CUDA if a CUDA call
  * failed, PA_ERR_INVALID_ARG for a null `bits` or a bad ordinal. */
 pa_status pa_noalloc_check_errors(int32_t device, void *stream, uint32_t *bits);
+
+/* ---- prompts and drafted tokens ----
+ *
+ * What a serving step does around the single-query decode: block tables and
+ * slots for new tokens from lengths that live on the GPU, the append of all of
+ * them at once, attention of whole prompts, and attention of a tree of drafted
+ * tokens.  Both attentions read the cache through block tables: the pool's own
+ * (`seqs`: host ids of n sequences; block_tables and kv_lens NULL) or the
+ * caller's (`block_tables`: device int32 [n][max_blocks_per_seq], such as
+ * pa_build_tables keeps, with `kv_lens`: host int32 [n]; seqs NULL).  Tables
+ * that the caller keeps are unknown to the pool's block manager: a pool whose
+ * blocks are handed out that way should not hand out blocks itself. */
+
+/* Extend the block tables of n requests from old_lens[i] to new_lens[i] tokens
+ * and list the cache slots of the new tokens, on the GPU.  All pointers are
+ * device int32 arrays.  With B = block_size:
+ *   - request i takes need_i = ceil(new/B) - ceil(old/B) ids of free_blocks
+ *     [num_free], in request order, starting at entry *free_head:
+ *     block_tables[i][ceil(old/B) + k] = its k-th id.  Other entries of
+ *     block_tables ([n][max_blocks_per_seq]) keep their values;
+ *   - *free_head_out = *free_head + sum of need_i (both pointers may name the
+ *     same word);
+ *   - cu_tokens[n + 1]: exclusive sums of new - old (cu_tokens[n] = all tokens);
+ *   - slots[cu_tokens[i] + j] = table entry of position old + j, times B, plus
+ *     (old + j) % B; slots from cu_tokens[n] up to slots_cap are -1, so a call
+ *     of a fixed size may carry fewer tokens.
+ * n <= 8192.  Checked on the device, reported by pa_check_device_errors:
+ * old < 0, new < old or new beyond max_blocks_per_seq * B sets
+ * PA_DEVERR_BAD_LEN and leaves that request as it is (no blocks, no tokens);
+ * more ids needed than free_blocks holds from *free_head on
+ * (PA_DEVERR_NO_BLOCKS), or more tokens than slots_cap (PA_DEVERR_BAD_LEN):
+ * nothing is taken -- tables and head stay, cu_tokens are 0, slots are -1; an
+ * id outside [0, num_blocks) among those of new tokens sets
+ * PA_DEVERR_BAD_BLOCK and gives slots of -1.
+ * Errors: PA_ERR_INVALID_ARG (null or misaligned pointer, n or a size out of
+ * range, host-only pool), PA_ERR_CUDA. */
+pa_status pa_build_tables(pa_pool *pool, int32_t n, const int32_t *old_lens, const int32_t *new_lens,
+                          const int32_t *free_blocks, int32_t num_free, const int32_t *free_head,
+                          int32_t *free_head_out, int32_t *block_tables, int32_t *cu_tokens,
+                          int32_t *slots, int32_t slots_cap, void *stream);
+
+/* pa_append_kv with the slots on the device: row t of k_new / v_new ([T]
+ * [num_kv_heads][head_dim] act_dtype) goes to slot slots[t] = block *
+ * block_size + offset of `layer`, stored as pa_append_kv stores it.  Slots of
+ * -1 are skipped; any other slot outside the pool is skipped and sets
+ * PA_DEVERR_BAD_BLOCK.  Slots of one call must be distinct, and the blocks they
+ * lie in are the caller's to know (no sharing check).
+ * Errors: PA_ERR_INVALID_ARG, PA_ERR_CUDA. */
+pa_status pa_append_kv_slots(pa_pool *pool, int32_t layer, int32_t T, const int32_t *slots,
+                             const void *k_new, const void *v_new, void *stream);
+
+/* Causal attention of the last q_lens[i] (host) tokens of each sequence: whole
+ * prompts (q_lens = lengths), or chunks behind a cached prefix.  The K/V rows of
+ * all of them are in the cache already (append first).  q / out: the query
+ * tokens of sequence 0, then 1, ... packed, [sum of q_lens][num_q_heads]
+ * [head_dim] act_dtype.  Token t of sequence i stands at position
+ * p = len - q_lens[i] + t and attends positions 0 .. p; everything else as
+ * pa_decode_attention (heads, group 1, 2, 4 or 8, FP8 scales, fp32 softmax and
+ * sums; the probabilities enter the second product rounded to act_dtype).
+ * q_lens[i] may be 0.  A sequence may be named twice.  Results do not depend on
+ * where the blocks lie.  Cache rows inside a sequence's length must be finite:
+ * a row that a token does not attend has weight 0 for it, and 0 x inf is NaN
+ * (slots past the length may hold anything).
+ * Errors: PA_ERR_INVALID_ARG, PA_ERR_NO_SEQ, PA_ERR_CUDA. */
+pa_status pa_prefill_attention(pa_pool *pool, int32_t layer, int32_t n, const int32_t *seqs,
+                               const int32_t *block_tables, const int32_t *kv_lens,
+                               const int32_t *q_lens, int32_t num_q_heads, const void *q, void *out,
+                               float scale, void *stream);
+
+/* Attention of drafted tokens: the last tree_lens[i] (host, 0 .. 64) tokens of
+ * sequence i are drafts in one tree.  Draft t attends every position before the
+ * drafts, and draft j if bit j of its word of tree_mask (device uint64, packed
+ * like q) is set -- its ancestors and itself for a tree; any mask is allowed,
+ * bits at or above tree_lens[i] do not count, and a draft that attends nothing
+ * gives zeros.  Other arguments, layout and errors as pa_prefill_attention. */
+pa_status pa_tree_attention(pa_pool *pool, int32_t layer, int32_t n, const int32_t *seqs,
+                            const int32_t *block_tables, const int32_t *kv_lens,
+                            const int32_t *tree_lens, const uint64_t *tree_mask,
+                            int32_t num_q_heads, const void *q, void *out, float scale, void *stream);
 
 /* Drop `seq`: every block's reference count falls by one, and blocks that
  * reach zero go to the tail of the free list in logical-block order ([MKV]

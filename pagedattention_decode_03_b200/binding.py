@@ -31,6 +31,7 @@ DTYPES = {"bf16": PA_BF16, "fp16": PA_FP16, "fp8_e4m3": PA_FP8_E4M3}
 PA_DEVERR_BAD_BLOCK = 0x1
 PA_DEVERR_BAD_LEN = 0x2
 PA_DEVERR_TIMEOUT = 0x4
+PA_DEVERR_NO_BLOCKS = 0x8
 
 # every symbol include/pa.h declares
 EXPORTS = (
@@ -42,7 +43,8 @@ EXPORTS = (
     "pa_plan_siblings", "pa_prefix_register", "pa_prefix_match", "pa_alloc_blocks_prefix",
     "pa_get_cached_blocks", "pa_swap_bytes", "pa_swap_out", "pa_swap_in",
     "pa_noalloc_check_errors", "pa_set_decode_path", "pa_last_decode_kernel",
-    "pa_state_size", "pa_state_save", "pa_state_load",
+    "pa_state_size", "pa_state_save", "pa_state_load", "pa_build_tables", "pa_append_kv_slots",
+    "pa_prefill_attention", "pa_tree_attention",
 )
 
 
@@ -107,6 +109,10 @@ def lib() -> ctypes.CDLL:
                                                   i32, vp, vp, ctypes.c_float, vp]
         L.pa_noalloc_check_errors.argtypes = [i32, vp, u32p]
         L.pa_noalloc_check_errors.restype = ctypes.c_int32
+        L.pa_build_tables.argtypes = [vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, vp]
+        L.pa_append_kv_slots.argtypes = [vp, i32, i32, vp, vp, vp, vp]
+        L.pa_prefill_attention.argtypes = [vp, i32, i32, vp, vp, vp, vp, i32, vp, vp, ctypes.c_float, vp]
+        L.pa_tree_attention.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, ctypes.c_float, vp]
         L.pa_free.argtypes = [vp, i32]
         L.pa_set_decode_path.argtypes = [vp, i32]
         L.pa_set_decode_path.restype = ctypes.c_int32
@@ -138,7 +144,8 @@ def lib() -> ctypes.CDLL:
         L.pa_status_string.restype = ctypes.c_char_p
         for name in ("pa_pool_create", "pa_alloc_blocks", "pa_alloc_blocks_n", "pa_fork_cow",
                      "pa_decode_attention_noalloc",
-                     "pa_append_kv", "pa_decode_attention", "pa_free", "pa_get_seq",
+                     "pa_append_kv", "pa_decode_attention", "pa_free", "pa_get_seq", "pa_build_tables",
+                     "pa_append_kv_slots", "pa_prefill_attention", "pa_tree_attention",
                      "pa_get_refcounts", "pa_get_free_list", "pa_get_cow_log",
                      "pa_check_device_errors", "pa_debug_fail_after"):
             getattr(L, name).restype = ctypes.c_int32
@@ -391,6 +398,112 @@ def pa_decode_attention_noalloc(desc: pa_pool_desc, layer: int, block_tables, se
                                              ctypes.c_void_p(qp), ctypes.c_void_p(op),
                                              ctypes.c_float(scale), _stream(stream)),
            "pa_decode_attention_noalloc")
+
+
+def _pool_stream(pool: Pool, stream):
+    """`stream`, or the pool's device's current one."""
+    if stream is not None:
+        return _stream(stream)
+    import torch
+    if not torch.cuda.is_available():
+        return ctypes.c_void_p(0)
+    return ctypes.c_void_p(torch.cuda.current_stream(pool.desc.device).cuda_stream)
+
+
+def _pool_tensor(pool: Pool, t, name: str, dtype, shape) -> int:
+    """Address of a contiguous tensor of this type and shape on the pool's device
+    (None in `shape`: any size there)."""
+    if not t.is_cuda or t.device.index != pool.desc.device or not t.is_contiguous() or t.dtype != dtype:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{pool.desc.device}")
+    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _act(pool: Pool):
+    import torch
+    return torch.bfloat16 if pool.act_dtype == "bf16" else torch.float16
+
+
+def pa_build_tables(pool: Pool, old_lens, new_lens, free_blocks, free_head, free_head_out, block_tables,
+                    cu_tokens, slots, stream=None) -> None:
+    """Extend device block tables from old_lens to new_lens tokens and list the new
+    tokens' slots, on the GPU.  All arguments are int32 device tensors: lengths [n],
+    free_blocks [F], free_head / free_head_out [1], block_tables [n][max_blocks_per_seq],
+    cu_tokens [n + 1], slots [capacity]."""
+    import torch
+    n = old_lens.shape[0] if old_lens.dim() == 1 else -1
+    i32 = torch.int32
+    ptrs = [_pool_tensor(pool, t, name, i32, shape) for t, name, shape in (
+        (old_lens, "old_lens", (n,)), (new_lens, "new_lens", (n,)), (free_blocks, "free_blocks", (None,)),
+        (free_head, "free_head", (1,)), (free_head_out, "free_head_out", (1,)),
+        (block_tables, "block_tables", (n, pool.max_blocks_per_seq)), (cu_tokens, "cu_tokens", (n + 1,)),
+        (slots, "slots", (None,)))]
+    old, new, free, head, head_out, tab, cu, sl = ptrs
+    _check(lib().pa_build_tables(pool.handle, n, old, new, free, free_blocks.shape[0], head, head_out, tab, cu,
+                                 sl, slots.shape[0], _pool_stream(pool, stream)), "pa_build_tables")
+
+
+def pa_append_kv_slots(pool: Pool, layer: int, slots, k_new, v_new, stream=None) -> None:
+    """Write row t of k_new / v_new [T][H_kv][128] to cache slot slots[t] (int32 device
+    tensor [T]; -1 skips the row) of `layer`."""
+    import torch
+    T = slots.shape[0] if slots.dim() == 1 else -1
+    shape = (T, pool.num_kv_heads, 128)
+    sp = _pool_tensor(pool, slots, "slots", torch.int32, (T,))
+    kp = _pool_tensor(pool, k_new, "k_new", _act(pool), shape)
+    vp = _pool_tensor(pool, v_new, "v_new", _act(pool), shape)
+    _check(lib().pa_append_kv_slots(pool.handle, layer, T, sp, kp, vp, _pool_stream(pool, stream)),
+           "pa_append_kv_slots")
+
+
+def _attend(fn, where: str, pool: Pool, layer: int, lens, mask, q, out, scale: float, seqs, kv_lens,
+            block_tables, stream) -> None:
+    import torch
+    m = _i32(lens)
+    n = len(m)
+    rows = int(m.sum(dtype=np.int64))
+    hq = q.shape[1] if q.dim() == 3 else -1
+    qp = _pool_tensor(pool, q, "q", _act(pool), (rows, hq, 128))
+    op = _pool_tensor(pool, out, "out", _act(pool), (rows, hq, 128))
+    s = tab = kl = None
+    if seqs is not None:
+        s = _i32(seqs)
+        if len(s) != n:
+            raise ValueError("seqs and the query lengths differ in length")
+    if kv_lens is not None:
+        kl = _i32(kv_lens)
+        if len(kl) != n:
+            raise ValueError("kv_lens and the query lengths differ in length")
+    if block_tables is not None:
+        tab = _pool_tensor(pool, block_tables, "block_tables", torch.int32, (n, pool.max_blocks_per_seq))
+    args = [pool.handle, layer, n, s.ctypes.data if s is not None else None, tab,
+            kl.ctypes.data if kl is not None else None, m.ctypes.data]
+    if mask is not None:
+        args.append(_pool_tensor(pool, mask, "tree_mask", mask.dtype, (rows,)))
+    _check(fn(*args, hq, qp, op, scale, _pool_stream(pool, stream)), where)
+
+
+def pa_prefill_attention(pool: Pool, layer: int, q_lens, q, out, scale: float, seqs=None, kv_lens=None,
+                         block_tables=None, stream=None) -> None:
+    """Causal attention of the last q_lens[i] tokens of each sequence over its cached
+    rows: q / out [sum(q_lens)][H_q][128].  The sequences are `seqs` of the pool, or
+    `block_tables` (device int32 [n][max_blocks_per_seq]) with host `kv_lens` [n]."""
+    _attend(lib().pa_prefill_attention, "pa_prefill_attention", pool, layer, q_lens, None, q, out, scale, seqs,
+            kv_lens, block_tables, stream)
+
+
+def pa_tree_attention(pool: Pool, layer: int, tree_lens, tree_mask, q, out, scale: float, seqs=None,
+                      kv_lens=None, block_tables=None, stream=None) -> None:
+    """Attention of the last tree_lens[i] <= 64 tokens of each sequence, drafts of one
+    tree: each attends the whole prefix and the drafts whose bits its word of
+    `tree_mask` (int64 or uint64 device tensor [sum(tree_lens)]) sets.  Other
+    arguments as pa_prefill_attention."""
+    import torch
+    if tree_mask.dtype not in (torch.int64, torch.uint64):
+        raise ValueError("tree_mask must be an int64 or uint64 tensor")
+    _attend(lib().pa_tree_attention, "pa_tree_attention", pool, layer, tree_lens, tree_mask, q, out, scale, seqs,
+            kv_lens, block_tables, stream)
 
 
 def pa_get_seq(pool: Pool, seq: int):

@@ -910,6 +910,176 @@ pa_status pa_decode_attention_append(pa_pool* p, int32_t layer, int32_t n, const
                      v_new);
 }
 
+pa_status pa_build_tables(pa_pool* p, int32_t n, const int32_t* old_lens, const int32_t* new_lens,
+                          const int32_t* free_blocks, int32_t num_free, const int32_t* free_head,
+                          int32_t* free_head_out, int32_t* block_tables, int32_t* cu_tokens, int32_t* slots,
+                          int32_t slots_cap, void* stream) {
+  PA_RANGE();
+  g_last_error.clear();
+  if (!p) return fail(PA_ERR_INVALID_ARG, "null pool");
+  if (p->host_only) return fail(PA_ERR_INVALID_ARG, "host-only pool: no device buffers");
+  if (n < 0 || n > pa::kTablesMaxSeqs) return fail(PA_ERR_INVALID_ARG, "n must be in [0, 8192]");
+  if (num_free < 0 || slots_cap < 0) return fail(PA_ERR_INVALID_ARG, "negative size");
+  if (!free_head || !free_head_out || !cu_tokens || (n > 0 && (!old_lens || !new_lens || !block_tables)) ||
+      (num_free > 0 && !free_blocks) || (slots_cap > 0 && !slots))
+    return fail(PA_ERR_INVALID_ARG, "null argument");
+  const void* ptrs[] = {old_lens, new_lens, free_blocks, free_head, free_head_out, block_tables, cu_tokens, slots};
+  for (const void* x : ptrs)
+    if (reinterpret_cast<uintptr_t>(x) & 3) return fail(PA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+  DeviceGuard guard(p->d.device);
+  if (!guard.ok) return fail(PA_ERR_CUDA, "cannot select the pool's device");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  pa_status st = ensure_device(p, s);
+  if (st != PA_OK) return st;
+  const cudaError_t e = pa::launch_build_tables(p->view, n, old_lens, new_lens, free_blocks, num_free, free_head,
+                                                free_head_out, block_tables, cu_tokens, slots, slots_cap,
+                                                p->num_sms, s);
+  if (e != cudaSuccess) return cuda_fail(e, "build tables launch");
+  ++p->launches;
+  pa::logf(2, "build_tables: %d requests, %d free ids, %d slots", n, num_free, slots_cap);
+  return PA_OK;
+}
+
+pa_status pa_append_kv_slots(pa_pool* p, int32_t layer, int32_t T, const int32_t* slots, const void* k_new,
+                             const void* v_new, void* stream) {
+  PA_RANGE();
+  g_last_error.clear();
+  if (!p) return fail(PA_ERR_INVALID_ARG, "null pool");
+  if (p->host_only) return fail(PA_ERR_INVALID_ARG, "host-only pool: no device buffers");
+  if (layer < 0 || layer >= p->d.num_layers) return fail(PA_ERR_INVALID_ARG, "layer out of range");
+  if (T < 0 || (T > 0 && (!slots || !k_new || !v_new))) return fail(PA_ERR_INVALID_ARG, "null argument");
+  if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15)
+    return fail(PA_ERR_INVALID_ARG, "k_new / v_new must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(slots) & 3) return fail(PA_ERR_INVALID_ARG, "slots must be 4-byte aligned");
+  if (T == 0) return PA_OK;
+  DeviceGuard guard(p->d.device);
+  if (!guard.ok) return fail(PA_ERR_CUDA, "cannot select the pool's device");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  pa_status st = ensure_device(p, s);
+  if (st != PA_OK) return st;
+  const cudaError_t e = pa::launch_append_slots(p->view, layer, T, slots, k_new, v_new, s);
+  if (e != cudaSuccess) return cuda_fail(e, "append launch");
+  ++p->launches;
+  pa::logf(2, "append_slots: layer %d, %d tokens", layer, T);
+  return PA_OK;
+}
+
+namespace {
+
+// pa_prefill_attention (mask null) and pa_tree_attention.
+pa_status attend_call(pa_pool* p, const char* what, bool tree, int32_t layer, int32_t n, const int32_t* seqs,
+                      const int32_t* block_tables, const int32_t* kv_lens, const int32_t* q_lens,
+                      const uint64_t* mask, int32_t num_q_heads, const void* q, void* out, float scale,
+                      void* stream) {
+  const std::string call(what);
+  if (!p) return fail(PA_ERR_INVALID_ARG, "null pool");
+  if (p->host_only) return fail(PA_ERR_INVALID_ARG, "host-only pool: no device buffers");
+  if (layer < 0 || layer >= p->d.num_layers) return fail(PA_ERR_INVALID_ARG, "layer out of range");
+  if (n < 0 || (n > 0 && !q_lens)) return fail(PA_ERR_INVALID_ARG, "null argument");
+  if (n > 0 && (seqs != nullptr) == (block_tables != nullptr))
+    return fail(PA_ERR_INVALID_ARG, call + ": give either seqs or block_tables");
+  if (n > 0 && (block_tables != nullptr) != (kv_lens != nullptr))
+    return fail(PA_ERR_INVALID_ARG, call + ": kv_lens go with block_tables (sequences of the pool have theirs)");
+  if (num_q_heads <= 0 || num_q_heads % p->d.num_kv_heads != 0)
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads must be a multiple of num_kv_heads");
+  const int32_t group = num_q_heads / p->d.num_kv_heads;
+  if (group != 1 && group != 2 && group != 4 && group != 8)
+    return fail(PA_ERR_INVALID_ARG, "query group (num_q_heads / num_kv_heads) must be 1, 2, 4 or 8");
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15)
+    return fail(PA_ERR_INVALID_ARG, "q / out must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(block_tables) & 3)
+    return fail(PA_ERR_INVALID_ARG, "block_tables must be 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(mask) & 7) return fail(PA_ERR_INVALID_ARG, "tree_mask must be 8-byte aligned");
+  if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale must be finite");
+  const int64_t max_len = static_cast<int64_t>(p->d.max_blocks_per_seq) * p->d.block_size;
+  int64_t total = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    int64_t len;
+    if (seqs) {
+      pa_status st = seq_arg(p, seqs[i]);
+      if (st != PA_OK) return st;
+      if (!p->bm->active(seqs[i])) return fail(PA_ERR_NO_SEQ, call + ": no such sequence");
+      len = p->bm->len(seqs[i]);
+    } else {
+      len = kv_lens[i];
+      if (len < 0 || len > max_len)
+        return fail(PA_ERR_INVALID_ARG, call + ": a length outside [0, max_blocks_per_seq * block_size]");
+    }
+    if (q_lens[i] < 0 || q_lens[i] > len)
+      return fail(PA_ERR_INVALID_ARG, call + ": query tokens must be in [0, cached tokens]");
+    if (tree && q_lens[i] > pa::kTreeMax)
+      return fail(PA_ERR_INVALID_ARG, call + ": at most 64 drafted tokens per sequence");
+    total += q_lens[i];
+  }
+  if (total * num_q_heads >= (int64_t{1} << 31))
+    return fail(PA_ERR_INVALID_ARG, call + ": query tokens * num_q_heads >= 2^31");
+  if (total == 0) return PA_OK;
+  if (!q || !out || (tree && !mask)) return fail(PA_ERR_INVALID_ARG, "null argument");
+  DeviceGuard guard(p->d.device);
+  if (!guard.ok) return fail(PA_ERR_CUDA, "cannot select the pool's device");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  pa_status st = ensure_device(p, s);
+  if (st != PA_OK) return st;
+  if (seqs) {
+    st = flush_deltas(p, s);
+    if (st != PA_OK) return st;
+  }
+  pa::AttendArgs args;
+  args.q = q;
+  args.out = out;
+  args.tables = seqs ? p->view.tables : block_tables;
+  args.mask = mask;
+  args.total_tokens = total;
+  args.layer = layer;
+  args.num_q_heads = num_q_heads;
+  args.scale = scale;
+  static thread_local pa::AttendItems items;
+  int32_t row = 0;
+  const uint64_t launches0 = p->launches;
+  for (int32_t at = 0; at < n;) {
+    items.n = 0;
+    items.row0 = row;
+    items.q0[0] = 0;
+    for (; at < n && items.n < pa::kAttendItemsCap; ++at) {
+      if (q_lens[at] == 0) continue;
+      const int32_t k = items.n++;
+      items.row[k] = seqs ? seqs[at] : at;
+      items.kv_len[k] = seqs ? p->bm->len(seqs[at]) : kv_lens[at];
+      items.q0[k + 1] = items.q0[k] + q_lens[at];
+    }
+    if (items.n == 0) break;
+    row += items.q0[items.n];
+    int launches = 0;
+    const cudaError_t e = pa::launch_attend(p->view, p->maps, args, items, p->num_sms, s, &launches);
+    p->launches += launches;
+    if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  }
+  pa::logf(2, "%s: layer %d, %d sequences, %lld query tokens, G=%d, %s tables, %llu launches", what, layer, n,
+           static_cast<long long>(total), group, seqs ? "the pool's" : "the caller's",
+           static_cast<unsigned long long>(p->launches - launches0));
+  return PA_OK;
+}
+
+}  // namespace
+
+pa_status pa_prefill_attention(pa_pool* p, int32_t layer, int32_t n, const int32_t* seqs,
+                               const int32_t* block_tables, const int32_t* kv_lens, const int32_t* q_lens,
+                               int32_t num_q_heads, const void* q, void* out, float scale, void* stream) {
+  PA_RANGE();
+  g_last_error.clear();
+  return attend_call(p, "pa_prefill_attention", false, layer, n, seqs, block_tables, kv_lens, q_lens, nullptr,
+                     num_q_heads, q, out, scale, stream);
+}
+
+pa_status pa_tree_attention(pa_pool* p, int32_t layer, int32_t n, const int32_t* seqs, const int32_t* block_tables,
+                            const int32_t* kv_lens, const int32_t* tree_lens, const uint64_t* tree_mask,
+                            int32_t num_q_heads, const void* q, void* out, float scale, void* stream) {
+  PA_RANGE();
+  g_last_error.clear();
+  return attend_call(p, "pa_tree_attention", true, layer, n, seqs, block_tables, kv_lens, tree_lens, tree_mask,
+                     num_q_heads, q, out, scale, stream);
+}
+
 pa_status pa_get_seq(pa_pool* p, int32_t seq, int32_t* len, int32_t* table, int32_t cap,
                      int32_t* nblocks) {
   PA_RANGE();

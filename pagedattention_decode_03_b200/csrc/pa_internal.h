@@ -27,6 +27,7 @@ constexpr int kMaxWorkers = 2048;     // warps of one decode launch (stream-K sl
 constexpr uint32_t kErrBadBlock = 0x1u;
 constexpr uint32_t kErrBadLen = 0x2u;
 constexpr uint32_t kErrTimeout = 0x4u;
+constexpr uint32_t kErrNoBlocks = 0x8u;
 
 // ---------------------------------------------------------------- pool view
 struct PoolView {
@@ -164,6 +165,44 @@ bool decode_tc_applies(int kv_dtype, int group);
 int decode_tc_worker_capacity(int num_sms);
 cudaError_t launch_decode_tc(const PoolView& pool, const CacheMaps& maps, const DecodePlan& plan,
                              const DecodeArgs& args, cudaStream_t stream);
+
+// ---------------------------------------------- prompts and drafted tokens
+// Block tables and the slot map from device request lengths (kernels_tables.cu).
+constexpr int kTablesMaxSeqs = 8192;
+cudaError_t launch_build_tables(const PoolView& pool, int n, const int32_t* old_lens, const int32_t* new_lens,
+                                const int32_t* free_blocks, int num_free, const int32_t* free_head,
+                                int32_t* free_head_out, int32_t* tables, int32_t* cu, int32_t* slots, int cap,
+                                int num_sms, cudaStream_t stream);
+
+// Append T rows to the slots a device map names (kernels_tables.cu).
+cudaError_t launch_append_slots(const PoolView& pool, int layer, int T, const int32_t* slots, const void* k_new,
+                                const void* v_new, cudaStream_t stream);
+
+// Attention of several query rows per sequence (kernels_attend.cu).
+constexpr int kAttendItemsCap = 512;
+constexpr int kTreeMax = 64;            // drafted tokens of one sequence
+
+struct AttendItems {
+  int32_t n;                            // items of this launch, each with at least one query token
+  int32_t row0;                         // packed row (token) of the first item's first token
+  int32_t row[kAttendItemsCap];         // row of `tables`
+  int32_t kv_len[kAttendItemsCap];      // cache positions, the query tokens' own last
+  int32_t q0[kAttendItemsCap + 1];      // prefix of the items' query tokens
+};
+
+struct AttendArgs {
+  const void* q;
+  void* out;
+  const int32_t* tables;                // [rows][mbps]
+  const uint64_t* mask;                 // tree mask per packed row; null: causal
+  int64_t total_tokens;                 // packed rows of q / out
+  int32_t layer;
+  int32_t num_q_heads;
+  float scale;
+};
+
+cudaError_t launch_attend(const PoolView& pool, const CacheMaps& maps, const AttendArgs& args,
+                          const AttendItems& items, int num_sms, cudaStream_t stream, int* launches);
 
 // Thread-local text returned by pa_last_error() (defined in api.cpp).
 void set_last_error(const std::string& msg);
