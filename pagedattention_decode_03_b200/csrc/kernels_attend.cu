@@ -1,15 +1,38 @@
 // Attention of several query rows per sequence over the paged cache: causal
 // prompts (pa_prefill_attention) and trees of drafted tokens
-// (pa_tree_attention).
+// (pa_tree_attention), on the 5th-generation tensor cores (tcgen05).
 //   out[t][h] = sum_p softmax_p(scale q[t][h] . k_p) v_p
 // over the cache positions p that token t of its sequence attends: all
 // positions up to its own (prompt), or the whole prefix and the drafted tokens
 // its mask names (tree).  A row that attends nothing gives zeros.
 //
-// One warp per (token, query head): 4 head dimensions a lane, the running
-// maximum and sum of the softmax in one pass over the positions.
+// A tile of queries is 128 rows of one KV head: 128 / G tokens x the G query
+// heads that share it (row = token * G + head in group), so a KV tile is read
+// once for the whole group and a tree's few tokens still fill rows.  Per tile
+// of 128 cache positions
+//   S[128 rows][128 positions] = Q K^T        (A, B from shared memory)
+//   O[128 rows][128 d]        += P V          (A = P from tensor memory,
+//                                              B = the V tile read MN-major)
+// with fp32 S and O in tensor memory; P, 16-bit, overlays S.  One CTA per SM
+// runs two softmax streams so that one stream's exponentials overlap the other
+// one's products:
+//   pair  the streams are two query tiles over the same KV tiles (256 rows a
+//         KV read: prompts, wide trees);
+//   dual  both streams serve one query tile and take every other KV tile; their
+//         results are joined in the epilogue (few rows: bound by the KV read).
+// Roles: warp 0 claims work and issues the TMA copies (one box per 16-token
+// block and d-half), warp 1 issues the MMAs, warps 4-7 and 8-11 are the two
+// softmax streams (a thread owns a row: its running maximum and sum need no
+// exchange), warps 12-15 convert FP8 codes to the activation type.
+// Work units are claimed from a counter, longest first.  Where there are too
+// few units for the SMs the positions are split into chunks whose partial
+// results (O, maximum, sum) a second kernel joins.
+// Every wait is bounded; one that gives up sets PA_DEVERR_TIMEOUT, and the CTA
+// waits for its copies and MMAs, frees its tensor memory and returns.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
+#include <mutex>
 
 #include "device_common.cuh"
 #include "pa_internal.h"
@@ -17,132 +40,987 @@
 namespace pa {
 namespace {
 
-struct AttendParams {
-  const uint8_t* q;
+constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTile = 128;                      // rows of a query tile, positions of a KV tile
+constexpr int kHalf = kTile * 128;              // one 64-element d-half of a 16-bit tile (16 KB)
+constexpr int kOperand = 2 * kHalf;             // a 16-bit tile (32 KB)
+constexpr int kRaw = kTile * 128;               // an FP8 tile (16 KB)
+constexpr int kPartFloats = kHeadDim + 2;       // of one row: O, maximum, sum
+constexpr float kLazy = 8.f;                    // log2 units a row's maximum may pass its reference by
+
+// Ring depths: up to 224 KB of the SM's 227.
+template <bool PAIR, bool FP8>
+struct Ring {
+  static constexpr int kQ = PAIR ? 2 : 1;
+  static constexpr int kStages = FP8 ? 3 : 5;
+  static constexpr int kRawStages = FP8 ? (PAIR ? 4 : 5) : 0;
+  static constexpr int kThreads = FP8 ? 512 : 384;
+  static constexpr int kOffKv = kQ * kOperand;
+  static constexpr int kOffRaw = kOffKv + kStages * kOperand;
+  static constexpr int kOffMeta = kOffRaw + kRawStages * kRaw;
+};
+
+// What the roles of a CTA know of a work unit.
+struct Unit {
+  int32_t seq_row;      // row of the block tables; < 0: no more work
+  int32_t h;            // KV head
+  int32_t tok0;         // packed row of the unit's first token
+  int32_t t0, m;        // first token within its sequence's query tokens, and their number
+  int32_t past, kv_len; // positions before the query tokens; all positions
+  int32_t tile0;        // first KV tile
+  int32_t n0, n1;       // KV tiles of stream 0 / 1 (dual: n0 = all tiles)
+  int32_t part;         // partial index of the unit (x kQ + stream)
+  int32_t direct;       // bit x: stream x has all its positions here and writes the output
+};
+
+struct Meta {
+  uint64_t kv_full[6], kv_empty[6], raw_full[6], raw_empty[6];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], ml[2];
+  uint64_t sched_full[2], sched_empty[2], done;
+  Unit unit[2];
+  uint32_t tmem;
+  int32_t abort;
+  int32_t rows[8][8];     // cache rows of the last 8 tiles' blocks
+  float mlv[2][2][2][kTile];  // [unit parity][stream][max, sum][row] (dual)
+};
+
+template <bool PAIR, bool FP8>
+constexpr size_t smem_bytes() {
+  return 1024 + Ring<PAIR, FP8>::kOffMeta + sizeof(Meta) - (PAIR ? sizeof(Meta::mlv) : 0);
+}
+
+struct Params {
   uint8_t* out;
-  const uint8_t* k_cache;
-  const uint8_t* v_cache;
   const int32_t* tables;
   const uint64_t* mask;     // tree: per packed row, or null (causal)
   const float* k_scale;
   const float* v_scale;
+  float* partials;
+  int32_t* counter;         // zero between launches
   uint32_t* err;
-  int64_t rows;             // (tokens of this launch) x query heads
   float sl2;                // scale * log2(e)
-  int32_t layer, H, G, num_blocks, mbps, bshift;
-  AttendItems items;
+  int32_t layer, H, gshift, num_blocks, mbps, bshift;  // gshift: log2(G); bshift: log2(block_size / 16)
+  int32_t units;            // work units, all heads
+  int32_t chunk;            // KV tiles of a chunk
+  int32_t part_rows;        // rows of a partial
+  int32_t n, row0;
+  int32_t row[kAttendItemsCap];
+  int32_t kv_len[kAttendItemsCap];
+  int32_t q0[kAttendItemsCap];       // first query token, and
+  int32_t m[kAttendItemsCap];        // how many
+  int32_t pre[kAttendItemsCap + 1];  // prefix of (query tiles x chunks), per KV head
 };
 
-template <int KV, int ACT>
-__device__ __forceinline__ void load4(const uint8_t* p, int64_t el, float (&x)[4]) {
-  if constexpr (KV == kFP8) {
-    const uint32_t r = *reinterpret_cast<const uint32_t*>(p + el);
-    const uint32_t a = dev::e4m3x2_to_f16x2(static_cast<uint16_t>(r)), b = dev::e4m3x2_to_f16x2(static_cast<uint16_t>(r >> 16));
-    x[0] = dev::f16lo_to_f32(a);
-    x[1] = dev::f16hi_to_f32(a);
-    x[2] = dev::f16lo_to_f32(b);
-    x[3] = dev::f16hi_to_f32(b);
-  } else {
-    const uint2 r = *reinterpret_cast<const uint2*>(p + el * 2);
-    if constexpr (ACT == kBF16) {
-      x[0] = dev::bf16lo_to_f32(r.x);
-      x[1] = dev::bf16hi_to_f32(r.x);
-      x[2] = dev::bf16lo_to_f32(r.y);
-      x[3] = dev::bf16hi_to_f32(r.y);
-    } else {
-      x[0] = dev::f16lo_to_f32(r.x);
-      x[1] = dev::f16hi_to_f32(r.x);
-      x[2] = dev::f16lo_to_f32(r.y);
-      x[3] = dev::f16hi_to_f32(r.y);
-    }
-  }
+// ------------------------------------------------------------------- tcgen05
+constexpr uint32_t kLayoutSW128 = 2;
+
+// Shared-memory operand: start address, leading and stride byte offsets in
+// 16-byte units, version 1, 128-byte swizzle.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t{1} << 46) |
+         (static_cast<uint64_t>(kLayoutSW128) << 61);
+}
+// kind::f16, fp32 accumulators, M = N = 128; B K-major or MN-major.
+__host__ __device__ constexpr uint32_t instr_desc(bool bf16, bool b_mn) {
+  return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) | (uint32_t(b_mn) << 16) |
+         (uint32_t(128 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of this thread's lane; the values are valid after tmem_wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t a, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(a)
+      : "memory");
+}
+// Waits for this thread's tensor-memory loads; v passes through, so no use of
+// it can be scheduled before the wait.
+__device__ __forceinline__ void tmem_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                 "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]),
+                 "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]),
+                 "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
+      "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]),
+      "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]),
+      "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-template <int KV, int ACT>
-__global__ void __launch_bounds__(256) attend_kernel(const __grid_constant__ AttendParams prm) {
-  dev::grid_dep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= prm.rows) return;
-  const int32_t hq = prm.H * prm.G;
-  const int32_t tok = static_cast<int32_t>(row / hq), qh = static_cast<int32_t>(row % hq), h = qh / prm.G;
-  const AttendItems& I = prm.items;
-  int lo = 0, hi = I.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (I.q0[mid] <= tok) lo = mid; else hi = mid - 1;
-  }
-  const int32_t t = tok - I.q0[lo], m = I.q0[lo + 1] - I.q0[lo], len = I.kv_len[lo], past = len - m;
-  const int32_t end = prm.mask ? len : past + t + 1;
-  const uint64_t mask = prm.mask ? prm.mask[I.row0 + tok] : 0;
-  float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, mx = -INFINITY, l = 0.f;
-  const int64_t qel = (static_cast<int64_t>(I.row0 + tok) * hq + qh) * kHeadDim + lane * 4;
-  load4<kBF16, ACT>(prm.q, qel, q);
-  const float sl2 = prm.sl2 * (KV == kFP8 ? prm.k_scale[prm.layer * prm.H + h] : 1.f);
-  const int32_t* table = prm.tables + static_cast<int64_t>(I.row[lo]) * prm.mbps;
-  for (int32_t p = 0; p < end; ++p) {
-    if (prm.mask && p >= past && !(mask >> (p - past) & 1)) continue;
-    int32_t phys = table[p >> prm.bshift];
-    if (static_cast<uint32_t>(phys) >= static_cast<uint32_t>(prm.num_blocks)) {
-      if (lane == 0) atomicOr(prm.err, kErrBadBlock);
-      phys = 0;
-    }
-    const int64_t el = ((((static_cast<int64_t>(prm.layer) * prm.num_blocks + phys) * prm.H + h) << prm.bshift) +
-                        (p & ((1 << prm.bshift) - 1))) * kHeadDim + lane * 4;
-    float k[4], v[4];
-    load4<KV, ACT>(prm.k_cache, el, k);
-    load4<KV, ACT>(prm.v_cache, el, v);
-    float s = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= sl2;
-    const float mn = fmaxf(mx, s);
-    const float c = mx == -INFINITY ? 0.f : dev::exp2_approx(mx - mn);
-    const float e = mn == -INFINITY ? 0.f : dev::exp2_approx(s - mn);
-    l = l * c + e;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) o[x] = o[x] * c + e * v[x];
-    mx = mn;
-  }
-  const float inv = (l > 0.f ? 1.f / l : 0.f) * (KV == kFP8 ? prm.v_scale[prm.layer * prm.H + h] : 1.f);
-  uint2 r;
-  if constexpr (ACT == kBF16)
-    r = make_uint2(dev::pack_bf16(o[0] * inv, o[1] * inv), dev::pack_bf16(o[2] * inv, o[3] * inv));
-  else
-    r = make_uint2(dev::pack_f16(o[0] * inv, o[1] * inv), dev::pack_f16(o[2] * inv, o[3] * inv));
-  *reinterpret_cast<uint2*>(prm.out + qel * 2) = r;
+template <int ACT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return ACT == kBF16 ? dev::pack_bf16(lo, hi) : dev::pack_f16(lo, hi);
 }
+
+// Columns of a 32-column chunk whose first n are allowed.
+__device__ __forceinline__ uint32_t low_bits(int32_t n) {
+  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// ------------------------------------------------------------------- kernel
+template <int KV, int ACT, bool PAIR>
+__global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
+    attend_kernel(const __grid_constant__ Params prm, const __grid_constant__ CUtensorMap tmk,
+                  const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq) {
+  constexpr bool kFp8 = KV == kFP8;
+  using R = Ring<PAIR, kFp8>;
+  constexpr int kLead = PAIR ? 1 : 2;           // K tiles copied ahead of the V tile of step i
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  Meta& mt = *reinterpret_cast<Meta*>(sm + R::kOffMeta);
+  const uint32_t base = dev::smem_u32(sm);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [](uint64_t& b) { return dev::smem_u32(&b); };
+  volatile int32_t* abort = &mt.abort;
+  constexpr int kSchedConsumers = 1 + 8 + (kFp8 ? 4 : 0);  // warps that read a unit
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 6; ++s) {
+      dev::mbar_init(bar(mt.kv_full[s]), kFp8 ? 4 : 1);
+      dev::mbar_init(bar(mt.kv_empty[s]), 1);
+      dev::mbar_init(bar(mt.raw_full[s]), 1);
+      dev::mbar_init(bar(mt.raw_empty[s]), 4);
+    }
+    for (int x = 0; x < 2; ++x) {
+      dev::mbar_init(bar(mt.q_full[x]), 1);
+      dev::mbar_init(bar(mt.q_empty[x]), 1);
+      dev::mbar_init(bar(mt.s_full[x]), 1);
+      dev::mbar_init(bar(mt.p_full[x]), 4);
+      dev::mbar_init(bar(mt.o_full[x]), 1);
+      dev::mbar_init(bar(mt.o_free[x]), PAIR ? 4 : 8);
+      dev::mbar_init(bar(mt.ml[x]), 4);
+      dev::mbar_init(bar(mt.sched_full[x]), 1);
+      dev::mbar_init(bar(mt.sched_empty[x]), kSchedConsumers);
+    }
+    dev::mbar_init(bar(mt.done), 1);
+    mt.abort = 0;
+    dev::fence_mbar_init();
+    dev::tma_prefetch_desc(&tmk);
+    dev::tma_prefetch_desc(&tmv);
+    dev::tma_prefetch_desc(&tmq);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dev::smem_u32(&mt.tmem)),
+                 "n"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&mt.tmem);
+  dev::grid_dep_wait();
+
+  // A warp's bounded wait, one outcome for all lanes; false ends the role.
+  auto wait = [&](uint64_t& b, uint32_t parity) {
+    const uint32_t a = dev::smem_u32(&b);
+    bool ok = false;
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+      if (dev::mbar_try_wait(a, parity)) {
+        ok = true;
+        break;
+      }
+      if (*abort) break;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok && lane == 0 && *abort == 0) {
+      *abort = 1;
+      atomicOr(prm.err, kErrTimeout);
+    }
+    return ok;
+  };
+  uint32_t unit_i = 0;
+  // The next unit, by the warps that consume the schedule.
+  auto next_unit = [&](Unit& u) {
+    if (!wait(mt.sched_full[unit_i & 1], (unit_i >> 1) & 1)) return false;
+    u = mt.unit[unit_i & 1];
+    __syncwarp();
+    if (lane == 0) arrive(bar(mt.sched_empty[unit_i & 1]));
+    ++unit_i;
+    return u.seq_row >= 0;
+  };
+
+  if (warp == 0) {
+    // ================================================================ producer
+    uint32_t ring_i = 0, sched_i = 0, q_i[2] = {0, 0};
+    int32_t w = blockIdx.x, w_next = 0;
+    bool ok = true;
+    const int32_t total = prm.units;
+    const int32_t tq = kTile >> prm.gshift;       // tokens of a query tile
+    for (;;) {
+      // the claim after this one is on its way while this unit is copied
+      if (lane == 0 && w < total) {
+        const int32_t v = atomicAdd(prm.counter, 1);
+        if (v == total - 1) *prm.counter = 0;     // the last claim of all: `units` claims in total
+        w_next = static_cast<int32_t>(gridDim.x) + v;
+      }
+      Unit u;
+      u.seq_row = -1;
+      const int32_t* table = prm.tables;
+      if (w < total) {
+        const int32_t wi = w / prm.H;
+        u.h = w - wi * prm.H;
+        int lo = 0, hi = prm.n - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (prm.pre[mid] <= wi) lo = mid; else hi = mid - 1;
+        }
+        u.seq_row = prm.row[lo];
+        u.m = prm.m[lo];
+        u.kv_len = prm.kv_len[lo];
+        u.past = u.kv_len - u.m;
+        const int32_t ut = tq * R::kQ;                               // tokens of a unit
+        const int32_t qt = (u.m + ut - 1) / ut;
+        const int32_t r = wi - prm.pre[lo], ch = (prm.pre[lo + 1] - prm.pre[lo]) / qt;
+        const int32_t c = r % ch;
+        u.t0 = (qt - 1 - r / ch) * ut;                               // the longest first
+        u.tok0 = prm.row0 + prm.q0[lo] + u.t0;
+        u.tile0 = c * prm.chunk;
+        u.part = w * R::kQ;
+        u.direct = 0;
+        int32_t nx[2] = {0, 0};
+#pragma unroll
+        for (int x = 0; x < R::kQ; ++x) {
+          if (u.t0 + x * tq >= u.m) break;
+          const int32_t last = prm.mask ? u.kv_len - 1 : u.past + min(u.t0 + (x + 1) * tq, u.m) - 1;
+          const int32_t nt = last / kTile + 1;
+          nx[x] = max(0, min(nt - u.tile0, prm.chunk));
+          if (nt <= prm.chunk) u.direct |= 1 << x;
+        }
+        u.n0 = nx[0];
+        u.n1 = nx[1];
+        table += static_cast<int64_t>(u.seq_row) * prm.mbps;
+      }
+      const int32_t n = u.seq_row < 0 ? 0 : max(u.n0, u.n1);
+      if (u.seq_row < 0 || n > 0) {                                  // an empty chunk is skipped
+        if (!(ok = wait(mt.sched_empty[sched_i & 1], ((sched_i >> 1) & 1) ^ 1))) break;
+        if (lane == 0) {
+          mt.unit[sched_i & 1] = u;
+          arrive(bar(mt.sched_full[sched_i & 1]));
+        }
+        ++sched_i;
+      }
+      if (u.seq_row < 0) break;
+      if (n > 0) {
+        // query tiles: [2 d-halves][128 rows][128 B], row = token * G + head
+#pragma unroll
+        for (int x = 0; x < R::kQ; ++x) {
+          if ((x == 0 ? u.n0 : u.n1) == 0) continue;
+          if (!(ok = wait(mt.q_empty[x], (q_i[x] & 1) ^ 1))) break;
+          if (lane == 0) {
+            const uint32_t dst = base + x * kOperand, b = bar(mt.q_full[x]);
+            dev::mbar_arrive_expect_tx(b, kOperand);
+            dev::tma_load_3d(dst, &tmq, 0, u.h << prm.gshift, u.tok0 + x * tq, b);
+            dev::tma_load_3d(dst + kHalf, &tmq, 64, u.h << prm.gshift, u.tok0 + x * tq, b);
+          }
+          ++q_i[x];
+        }
+        if (!ok) break;
+        // KV tiles: K(0..kLead-1), then V(i), K(i + kLead), ...
+        const int32_t blocks = (u.kv_len + 15) >> 4;                 // of 16 tokens
+        int32_t id = 0;
+        int32_t id_base = -64;
+        auto copy = [&](int32_t i, bool is_v) {
+          const int32_t b0 = (u.tile0 + i) * 8, nb = min(8, blocks - b0);
+          if (!is_v) {  // the tile's cache rows, kept for its V copy
+            if (b0 >= id_base + 32 || id_base < 0) {
+              id_base = b0;
+              const int32_t b = b0 + lane, e = b >> prm.bshift;
+              int32_t v = b < blocks && e < prm.mbps ? table[e] : 0;
+              if (static_cast<uint32_t>(v) >= static_cast<uint32_t>(prm.num_blocks)) {
+                atomicOr(prm.err, kErrBadBlock);
+                v = 0;
+              }
+              id = (((prm.layer * prm.num_blocks + v) * prm.H + u.h) << (4 + prm.bshift)) +
+                   (b & ((1 << prm.bshift) - 1)) * 16;
+            }
+            const int32_t row = __shfl_sync(0xffffffffu, id, (b0 - id_base + lane) & 31);
+            if (lane < 8) mt.rows[i & 7][lane] = row;
+            __syncwarp();
+          }
+          const CUtensorMap* map = is_v ? &tmv : &tmk;
+          constexpr int kDepth = kFp8 ? R::kRawStages : R::kStages;
+          const uint32_t st = ring_i % kDepth, par = ((ring_i / kDepth) & 1) ^ 1;
+          if (!wait(kFp8 ? mt.raw_empty[st] : mt.kv_empty[st], par)) return false;
+          const uint32_t full = bar(kFp8 ? mt.raw_full[st] : mt.kv_full[st]);
+          if (lane == 0) dev::mbar_arrive_expect_tx(full, nb * (kFp8 ? 2048 : 4096));
+          __syncwarp();  // the bytes are expected before any copy is issued
+          const int j = lane & 7, half = lane >> 3;
+          if (j < nb && half < (kFp8 ? 1 : 2)) {
+            const uint32_t dst = base + (kFp8 ? R::kOffRaw + st * kRaw : R::kOffKv + st * kOperand) + half * kHalf + j * 2048;
+            dev::tma_load_2d(dst, map, half * 64, mt.rows[i & 7][j], full);
+          }
+          ++ring_i;
+          return true;
+        };
+        for (int32_t i = 0; ok && i < min(kLead, n); ++i) ok = copy(i, false);
+        for (int32_t i = 0; ok && i < n; ++i) {
+          ok = copy(i, true);
+          if (ok && i + kLead < n) ok = copy(i + kLead, false);
+        }
+        if (!ok) break;
+      }
+      w = __shfl_sync(0xffffffffu, w_next, 0);
+    }
+    dev::grid_dep_launch();
+    // copies already issued land before the CTA can exit
+    constexpr uint32_t kDepth = kFp8 ? R::kRawStages : R::kStages;
+    for (uint32_t k = ring_i > kDepth ? ring_i - kDepth : 0; k < ring_i; ++k)
+      dev::mbar_wait_bounded(bar(kFp8 ? mt.raw_full[k % kDepth] : mt.kv_full[k % kDepth]), (k / kDepth) & 1, kWaitLimit);
+    for (int x = 0; x < R::kQ; ++x)
+      if (q_i[x]) dev::mbar_wait_bounded(bar(mt.q_full[x]), (q_i[x] - 1) & 1, kWaitLimit);
+  } else if (warp == 1) {
+    // ===================================================================== MMA
+    constexpr bool kBf = ACT == kBF16;
+    constexpr uint32_t kIdS = instr_desc(kBf, false), kIdO = instr_desc(kBf, true);
+    uint32_t kv_i = 0, q_i[2] = {0, 0}, p_i[2] = {0, 0}, o_i[2] = {0, 0};
+    Unit u;
+    bool ok = true;
+    while (ok && next_unit(u)) {
+      const int32_t n = max(u.n0, u.n1);
+      // ring positions of the unit's K and V tiles
+      auto pos_k = [&](int32_t i) { return PAIR ? 2 * i : (i == 0 ? 0 : 2 * i - 1); };
+      auto pos_v = [&](int32_t i) { return PAIR ? 2 * i + 1 : (i == n - 1 ? 2 * n - 1 : 2 * i + 2); };
+      auto kv_wait = [&](int32_t pos) {
+        const uint32_t k = kv_i + pos;
+        return wait(mt.kv_full[k % R::kStages], (k / R::kStages) & 1);
+      };
+      auto kv_release = [&](int32_t pos) {
+        if (lane == 0) commit(bar(mt.kv_empty[(kv_i + pos) % R::kStages]));
+      };
+      auto stage = [&](int32_t pos) { return base + R::kOffKv + ((kv_i + pos) % R::kStages) * kOperand; };
+      auto issue_s = [&](int x, int32_t i) {
+        fence_after();
+        if (lane == 0) {
+          const uint32_t qa = base + (PAIR ? x : 0) * kOperand, ka = stage(pos_k(i));
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
+            mma_ss(tmem + x * 128, smem_desc(qa + o, 16, 1024), smem_desc(ka + o, 16, 1024), kIdS, kk > 0);
+          }
+          commit(bar(mt.s_full[x]));
+        }
+        __syncwarp();
+      };
+      auto issue_pv = [&](int x, int32_t i, bool acc) {
+        fence_after();
+        if (lane == 0) {
+          const uint32_t va = stage(pos_v(i));
+          const int32_t steps = min(8, ((u.kv_len + 15) >> 4) - (u.tile0 + i) * 8);  // 16-token blocks copied
+          for (int j = 0; j < steps; ++j)
+            mma_ts(tmem + 256 + x * 128, tmem + x * 128 + j * 8, smem_desc(va + j * 2048, kHalf, 1024), kIdO,
+                   acc || j > 0);
+        }
+        __syncwarp();
+      };
+      // V rows past the length: their weights are 0, and 0 x NaN is NaN
+      auto clean_v = [&](int32_t i) {
+        if constexpr (!kFp8) {
+          const int32_t valid = u.kv_len - (u.tile0 + i) * kTile;
+          if (valid < kTile && (valid & 15)) {
+            uint8_t* v = sm + (stage(pos_v(i)) - base);
+            const int32_t rows = 16 - (valid & 15);
+            for (int c = lane; c < rows * 16; c += 32)
+              *reinterpret_cast<uint4*>(v + (c & 1) * kHalf + (valid + (c >> 4)) * 128 + ((c >> 1) & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            dev::fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+      };
+      if constexpr (PAIR) {
+        const int32_t nx[2] = {u.n0, u.n1};
+        if (!(ok = kv_wait(pos_k(0)))) break;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || nx[x] == 0) continue;
+          if (!(ok = wait(mt.q_full[x], q_i[x] & 1))) break;
+          ++q_i[x];
+          issue_s(x, 0);
+          if (nx[x] == 1 && lane == 0) commit(bar(mt.q_empty[x]));
+        }
+        if (!ok) break;
+        kv_release(pos_k(0));
+        for (int32_t j = 0; ok && j < n; ++j) {
+          if (!(ok = kv_wait(pos_v(j)))) break;
+          clean_v(j);
+          if (j + 1 < n && !(ok = kv_wait(pos_k(j + 1)))) break;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || j >= nx[x]) continue;
+            if (j == 0) {
+              if (!(ok = wait(mt.o_free[x], (o_i[x] & 1) ^ 1))) break;
+              ++o_i[x];
+            }
+            if (!(ok = wait(mt.p_full[x], p_i[x] & 1))) break;
+            ++p_i[x];
+            issue_pv(x, j, j > 0);
+            if (j == nx[x] - 1 && lane == 0) commit(bar(mt.o_full[x]));
+            if (x == 1 || j >= nx[1]) kv_release(pos_v(j));
+            if (j + 1 < nx[x]) {
+              issue_s(x, j + 1);
+              if (j + 1 == nx[x] - 1 && lane == 0) commit(bar(mt.q_empty[x]));
+            }
+            if (j + 1 < n && (x == 1 || j >= nx[1])) kv_release(pos_k(j + 1));
+          }
+        }
+      } else {
+        if (!(ok = wait(mt.q_full[0], q_i[0] & 1))) break;
+        ++q_i[0];
+        for (int32_t i = 0; ok && i < min(2, n); ++i) {
+          if (!(ok = kv_wait(pos_k(i)))) break;
+          issue_s(i, i);
+          kv_release(pos_k(i));
+          if (i == n - 1 && lane == 0) commit(bar(mt.q_empty[0]));
+        }
+        if (!ok) break;
+        if (!(ok = wait(mt.o_free[0], (o_i[0] & 1) ^ 1))) break;
+        ++o_i[0];
+        for (int32_t i = 0; i < n; ++i) {
+          const int x = i & 1;
+          if (!(ok = kv_wait(pos_v(i)))) break;
+          clean_v(i);
+          if (!(ok = wait(mt.p_full[x], p_i[x] & 1))) break;
+          ++p_i[x];
+          issue_pv(x, i, i > 1);
+          kv_release(pos_v(i));
+          if (i >= n - 2 && lane == 0) commit(bar(mt.o_full[x]));
+          if (i + 2 < n) {
+            if (!(ok = kv_wait(pos_k(i + 2)))) break;
+            issue_s(x, i + 2);
+            kv_release(pos_k(i + 2));
+            if (i + 2 == n - 1 && lane == 0) commit(bar(mt.q_empty[0]));
+          }
+        }
+      }
+      kv_i += 2 * n;
+    }
+    // every MMA issued has finished before the tensor memory is released
+    if (lane == 0) commit(bar(mt.done));
+    __syncwarp();
+    dev::mbar_wait_bounded(bar(mt.done), 0, kWaitLimit);
+  } else if (warp >= 4 && warp < 12) {
+    // ======================================================= softmax, epilogue
+    const int x = (warp >> 2) - 1;                     // stream
+    const int r = (warp & 3) * 32 + lane;              // row, and TMEM lane
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t ts = tl + x * 128, to = tl + 256 + x * 128;
+    const int32_t tq = kTile >> prm.gshift, G = 1 << prm.gshift;
+    uint32_t s_i = 0, o_i[2] = {0, 0}, ml_i = 0;
+    Unit u;
+    while (next_unit(u)) {
+      const int32_t n = PAIR ? (x == 0 ? u.n0 : u.n1) : u.n0;   // this stream's last step + 1
+      if (PAIR && n == 0) continue;
+      const int32_t t = u.t0 + (PAIR ? x : 0) * tq + (r >> prm.gshift), g = r & (G - 1);
+      const bool row_ok = t < u.m;
+      const bool warp_ok = u.t0 + (PAIR ? x : 0) * tq + (((warp & 3) * 32) >> prm.gshift) < u.m;
+      const int32_t tc = min(t, u.m - 1);               // rows behind the last token read its limits
+      const int32_t tok = u.tok0 + (t - u.t0);
+      uint64_t bits = 0;
+      int32_t lim;        // causal: positions allowed; tree: prefix positions, all allowed
+      if (prm.mask) {
+        lim = u.past;
+        bits = prm.mask[u.tok0 + (tc - u.t0)];
+        if (u.m < 64) bits &= (uint64_t{1} << u.m) - 1;
+      } else {
+        lim = u.past + tc + 1;
+      }
+      const int32_t lim_min = __reduce_min_sync(0xffffffffu, lim);
+      float sl2 = prm.sl2, vs = 1.f;
+      if constexpr (kFp8) {
+        sl2 *= prm.k_scale[prm.layer * prm.H + u.h];
+        vs = prm.v_scale[prm.layer * prm.H + u.h];
+      }
+      const bool neg = sl2 < 0.f;
+      const float asl2 = fabsf(sl2);
+      float mref = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int32_t i = PAIR ? 0 : x; i < n; i += PAIR ? 1 : 2) {
+        if (!(ok = wait(mt.s_full[x], s_i & 1))) break;
+        ++s_i;
+        fence_after();
+        if (warp_ok) {
+          const int32_t p0 = (u.tile0 + i) * kTile;
+          const bool masked = p0 + kTile > lim_min;
+          // allowed columns of chunk c
+          auto allowed = [&](int c) {
+            const int32_t k = lim - (p0 + c * 32);
+            uint32_t a = low_bits(k);
+            if (prm.mask && k < 32) a |= k >= 0 ? static_cast<uint32_t>(bits << k) : (k > -64 ? static_cast<uint32_t>(bits >> -k) : 0u);
+            return a;
+          };
+          float v[2][32];
+          float mx = -INFINITY;
+          tmem_ld32(ts, v[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_wait(v[c & 1]);
+            if (c < 3) tmem_ld32(ts + (c + 1) * 32, v[(c + 1) & 1]);
+            float(&y)[32] = v[c & 1];
+            if (masked) {
+              const uint32_t a = allowed(c);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (a >> k & 1) mx = fmaxf(mx, neg ? -y[k] : y[k]);
+            } else if (neg) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, -y[k]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, y[k]);
+            }
+          }
+          mx *= asl2;      // -inf where nothing is allowed (NaN for a zero scale)
+          if (!(mx >= -3.0e38f)) mx = asl2 == 0.f ? 0.f : -INFINITY;
+          tmem_ld32(ts, v[0]);
+          // the reference moves only when the maximum passes it by 2^8: O is
+          // then scaled, after the P V of the step before (complete: S came after it)
+          const bool move = mx > mref + kLazy || (mref == -INFINITY && mx > -INFINITY);
+          float corr = 1.f;
+          if (move) {
+            corr = mref == -INFINITY ? 0.f : dev::exp2_approx(mref - mx);
+            mref = mx;
+            l *= corr;
+          }
+          const bool first = i < (PAIR ? 1 : 2);
+          if (!first && __any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float o[32];
+              tmem_ld32(to + c * 32, o);
+              tmem_wait(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= corr;
+              tmem_st32(to + c * 32, o);
+            }
+          }
+          const float mr = mref == -INFINITY ? 0.f : mref;
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_wait(v[c & 1]);
+            if (c < 3) tmem_ld32(ts + (c + 1) * 32, v[(c + 1) & 1]);
+            float(&y)[32] = v[c & 1];
+            const uint32_t a = masked ? allowed(c) : 0xffffffffu;
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float e0 = dev::exp2_approx(fmaf(y[k], sl2, -mr)), e1 = dev::exp2_approx(fmaf(y[k + 1], sl2, -mr));
+              if (masked) {
+                e0 = a >> k & 1 ? e0 : 0.f;
+                e1 = a >> (k + 1) & 1 ? e1 : 0.f;
+              }
+              ls[(k >> 1) & 3] += e0 + e1;
+              pk[k >> 1] = pack2<ACT>(e0, e1);
+            }
+            // P overlays S: chunk c goes to columns 16c .. 16c + 15, of S chunk c / 2
+            tmem_st16(ts + c * 16, pk);
+          }
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          tmem_wait_st();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(bar(mt.p_full[x]));
+      }
+      if (!ok) break;
+      // ---- epilogue
+      uint16_t* out = reinterpret_cast<uint16_t*>(prm.out) +
+                      ((static_cast<int64_t>(tok) * prm.H + u.h) * G + g) * kHeadDim;
+      float* part = prm.partials + (static_cast<int64_t>(u.part + (PAIR ? x : 0)) * prm.part_rows + r) * kPartFloats;
+      const bool direct = u.direct >> (PAIR ? x : 0) & 1;
+      auto put = [&](int c, const float (&o)[32]) {  // columns 32c.. of this row
+        if (!row_ok) return;
+        if (direct) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4*>(out + c * 32 + k) =
+                make_uint4(pack2<ACT>(o[k], o[k + 1]), pack2<ACT>(o[k + 2], o[k + 3]), pack2<ACT>(o[k + 4], o[k + 5]),
+                           pack2<ACT>(o[k + 6], o[k + 7]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) *reinterpret_cast<float2*>(part + c * 32 + k) = make_float2(o[k], o[k + 1]);
+        }
+      };
+      if constexpr (PAIR) {
+        if (!wait(mt.o_full[x], o_i[x] & 1)) break;
+        ++o_i[x];
+        fence_after();
+        const float f = vs * (direct ? (l > 0.f ? 1.f / l : 0.f) : 1.f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+          tmem_ld32(to + c * 32, o);
+          tmem_wait(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = l > 0.f ? o[k] * f : 0.f;
+          put(c, o);
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(bar(mt.o_free[x]));
+        if (!direct && row_ok) *reinterpret_cast<float2*>(part + kHeadDim) = make_float2(mref, l);
+      } else {
+        // join the two streams; stream x writes d-half x
+        bool all = true;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          if (all && y < n) {
+            all = wait(mt.o_full[y], o_i[y] & 1);
+            ++o_i[y];
+          }
+        if (!all) break;
+        fence_after();
+        float(&mlv)[2][2][kTile] = mt.mlv[ml_i & 1];
+        mlv[x][0][r] = mref;
+        mlv[x][1][r] = l;
+        __syncwarp();
+        if (lane == 0) arrive(bar(mt.ml[x]));
+        if (!wait(mt.ml[x ^ 1], ml_i & 1)) break;
+        ++ml_i;
+        const float m2 = mlv[x ^ 1][0][r], l2 = mlv[x ^ 1][1][r];
+        const float mm = fmaxf(mref, m2);
+        float w0 = l > 0.f ? dev::exp2_approx(mref - mm) : 0.f, w1 = l2 > 0.f ? dev::exp2_approx(m2 - mm) : 0.f;
+        const float lsum = l * w0 + l2 * w1;
+        const float f = vs * (direct ? (lsum > 0.f ? 1.f / lsum : 0.f) : 1.f);
+        w0 *= f;
+        w1 *= f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float a[32], b[32];
+          tmem_ld32(to + x * 64 + c * 32, a);
+          tmem_ld32(tl + 256 + (x ^ 1) * 128 + x * 64 + c * 32, b);
+          tmem_wait(a);
+          tmem_wait(b);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) a[k] = (w0 != 0.f ? a[k] * w0 : 0.f) + (w1 != 0.f ? b[k] * w1 : 0.f);
+          put(x * 2 + c, a);
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(bar(mt.o_free[0]));
+        if (!direct && row_ok && x == 0) *reinterpret_cast<float2*>(part + kHeadDim) = make_float2(mm, lsum);
+      }
+    }
+  } else if (kFp8 && warp >= 12) {
+    // ================================================ FP8 codes to 16-bit tiles
+    uint32_t raw_i = 0;
+    const int tid = threadIdx.x - 384;
+    Unit u;
+    bool ok = true;
+    while (ok && next_unit(u)) {
+      const int32_t n = max(u.n0, u.n1);
+      auto convert = [&](int32_t i, bool is_v) {
+        const uint32_t rs = raw_i % (kFp8 ? R::kRawStages : 1), ks = raw_i % R::kStages;
+        if (!wait(mt.raw_full[rs], (raw_i / (kFp8 ? R::kRawStages : 1)) & 1)) return false;
+        if (!wait(mt.kv_empty[ks], ((raw_i / R::kStages) & 1) ^ 1)) return false;
+        const int32_t valid = min(kTile, u.kv_len - (u.tile0 + i) * kTile);
+        const uint8_t* src = sm + R::kOffRaw + rs * kRaw;
+        uint8_t* dst = sm + R::kOffKv + ks * kOperand;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int e = k * 128 + tid, tok = e >> 3, c = e & 7;      // 16 codes: 16c .. of token tok
+          uint4 raw = *reinterpret_cast<const uint4*>(src + tok * 128 + ((c ^ (tok & 7)) << 4));
+          if (is_v && tok >= valid) raw = make_uint4(0, 0, 0, 0);
+          const uint32_t wsrc[4] = {raw.x, raw.y, raw.z, raw.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint32_t h2 = dev::e4m3x2_to_f16x2(static_cast<uint16_t>(wsrc[q >> 1] >> ((q & 1) * 16)));
+            o[q] = ACT == kBF16 ? dev::pack_bf16(dev::f16lo_to_f32(h2), dev::f16hi_to_f32(h2)) : h2;
+          }
+          uint8_t* row = dst + (c >> 2) * kHalf + tok * 128;
+          const int cc = 2 * (c & 3), sw = tok & 7;
+          // the two d-halves write their chunks in opposite order: no bank is hit twice
+          const int f = c >> 2;
+          const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+          *reinterpret_cast<uint4*>(row + (((cc + f) ^ sw) << 4)) = f ? hi : lo;
+          *reinterpret_cast<uint4*>(row + (((cc + 1 - f) ^ sw) << 4)) = f ? lo : hi;
+        }
+        dev::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          arrive(bar(mt.kv_full[ks]));
+          arrive(bar(mt.raw_empty[rs]));
+        }
+        ++raw_i;
+        return true;
+      };
+      for (int32_t i = 0; ok && i < min(kLead, n); ++i) ok = convert(i, false);
+      for (int32_t i = 0; ok && i < n; ++i) {
+        ok = convert(i, true);
+        if (ok && i + kLead < n) ok = convert(i + kLead, false);
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+}
+
+// ------------------------------------------------------------- joining chunks
+// One warp per (token, query head) of a sequence that was split: the chunks'
+// O are weighted by 2^(their maximum - the row's) and divided by the sum.
+template <int ACT>
+__global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant__ Params prm, int tokens, int kq) {
+  dev::grid_dep_wait();
+  dev::grid_dep_launch();
+  const int lane = threadIdx.x & 31, G = 1 << prm.gshift, hq = prm.H << prm.gshift;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= static_cast<int64_t>(tokens) * hq) return;
+  const int32_t k = static_cast<int32_t>(row / hq), qh = static_cast<int32_t>(row % hq);
+  const int32_t h = qh >> prm.gshift, g = qh & (G - 1);
+  // items lie in the order of their work, not of their tokens: find the one that holds token k
+  int it = -1;
+  for (int i0 = 0; i0 < prm.n && it < 0; i0 += 32) {
+    const int i = i0 + lane;
+    const unsigned hit = __ballot_sync(0xffffffffu, i < prm.n && prm.q0[min(i, prm.n - 1)] <= k &&
+                                                        k < prm.q0[min(i, prm.n - 1)] + prm.m[min(i, prm.n - 1)]);
+    if (hit) it = i0 + __ffs(hit) - 1;
+  }
+  if (it < 0) return;
+  const int32_t tq = kTile >> prm.gshift, ut = tq * kq;
+  const int32_t t = k - prm.q0[it], m = prm.m[it], past = prm.kv_len[it] - m;
+  const int32_t tile = t / ut, x = (t - tile * ut) / tq;
+  const int32_t last = prm.mask ? prm.kv_len[it] - 1 : past + min(tile * ut + (x + 1) * tq, m) - 1;
+  const int32_t nt = last / kTile + 1;
+  if (nt <= prm.chunk) return;                    // written by its only chunk
+  const int32_t chunks = (nt + prm.chunk - 1) / prm.chunk;
+  const int32_t qt = (m + ut - 1) / ut, ch = (prm.pre[it + 1] - prm.pre[it]) / qt;
+  const int64_t w0 = (static_cast<int64_t>(prm.pre[it]) + (qt - 1 - tile) * ch) * prm.H + h;
+  const int32_t r = (t - tile * ut - x * tq) * G + g;
+  auto at = [&](int c) {
+    return prm.partials + (((w0 + static_cast<int64_t>(c) * prm.H) * kq + x) * prm.part_rows + r) * kPartFloats;
+  };
+  float mx = -INFINITY;
+  for (int c = lane; c < chunks; c += 32) mx = fmaxf(mx, __ldcg(at(c) + kHeadDim));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+  for (int c = 0; c < chunks; ++c) {
+    const float* p = at(c);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + kHeadDim));
+    if (ml.y > 0.f) {
+      const float w = dev::exp2_approx(ml.x - mx);
+      const float2 a = __ldcg(reinterpret_cast<const float2*>(p) + lane * 2);
+      const float2 b = __ldcg(reinterpret_cast<const float2*>(p) + lane * 2 + 1);
+      l += w * ml.y;
+      o[0] += w * a.x;
+      o[1] += w * a.y;
+      o[2] += w * b.x;
+      o[3] += w * b.y;
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint16_t* out = reinterpret_cast<uint16_t*>(prm.out) + ((static_cast<int64_t>(prm.row0) + k) * hq + qh) * kHeadDim;
+  *reinterpret_cast<uint2*>(out + lane * 4) =
+      make_uint2(pack2<ACT>(o[0] * inv, o[1] * inv), pack2<ACT>(o[2] * inv, o[3] * inv));
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encoder() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+template <int KV, int ACT, bool PAIR>
+cudaError_t run(const Params& prm, const CacheMaps& maps, const CUtensorMap& tmq, int num_sms, cudaStream_t stream) {
+  using R = Ring<PAIR, KV == kFP8>;
+  constexpr size_t smem = smem_bytes<PAIR, KV == kFP8>();
+  static_assert(smem <= 227 * 1024, "attention exceeds the shared memory of an SM");
+  static uint64_t configured = 0;  // bit per device: dynamic shared memory attribute set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(configured >> dev & 1u)) {
+    e = cudaFuncSetAttribute(attend_kernel<KV, ACT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) configured |= uint64_t{1} << dev;
+  }
+  return launch_pdl(attend_kernel<KV, ACT, PAIR>, dim3(std::min(num_sms, prm.units)), dim3(R::kThreads), smem, stream,
+                    prm, maps.k, maps.v, tmq);
+}
+
+template <bool PAIR>
+cudaError_t dispatch(const PoolView& pool, const Params& prm, const CacheMaps& maps, const CUtensorMap& tmq,
+                     int num_sms, cudaStream_t stream) {
+  const bool bf = pool.act_dtype == kBF16;
+  if (pool.kv_dtype == kFP8)
+    return bf ? run<kFP8, kBF16, PAIR>(prm, maps, tmq, num_sms, stream)
+              : run<kFP8, kFP16, PAIR>(prm, maps, tmq, num_sms, stream);
+  return bf ? run<kBF16, kBF16, PAIR>(prm, maps, tmq, num_sms, stream)
+            : run<kFP16, kFP16, PAIR>(prm, maps, tmq, num_sms, stream);
+}
+
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 }  // namespace
 
-cudaError_t launch_attend(const PoolView& pool, const CacheMaps&, const AttendArgs& a, const AttendItems& items,
+cudaError_t launch_attend(const PoolView& pool, const CacheMaps& maps, const AttendArgs& a, const AttendItems& items,
                           int num_sms, cudaStream_t stream, int* launches) {
-  static thread_local AttendParams prm;
-  prm.q = static_cast<const uint8_t*>(a.q);
+  EncodeTiledFn encode = encoder();
+  if (!encode) return cudaErrorNotSupported;
+  static thread_local Params prm;
+  static thread_local int order[kAttendItemsCap];
+  const int H = pool.num_kv_heads, G = a.num_q_heads / H;
+  const int tq = kTile / G;
+  const int n = items.n;
+  // units of one KV head, and the widest sequence, in each form
+  int64_t pair_units = 0;
+  int max_rows = 0;
+  for (int i = 0; i < n; ++i) {
+    const int m = items.q0[i + 1] - items.q0[i];
+    pair_units += ceil_div(m, 2 * tq);
+    max_rows = std::max(max_rows, m * G);
+  }
+  const bool pair = max_rows > kTile && pair_units * H >= num_sms;
+  const int kq = pair ? 2 : 1, ut = tq * kq;
+
   prm.out = static_cast<uint8_t*>(a.out);
-  prm.k_cache = static_cast<const uint8_t*>(pool.k_cache);
-  prm.v_cache = static_cast<const uint8_t*>(pool.v_cache);
   prm.tables = a.tables;
   prm.mask = a.mask;
   prm.k_scale = pool.k_scale;
   prm.v_scale = pool.v_scale;
+  prm.partials = pool.partials;
+  prm.counter = pool.counters;
   prm.err = pool.err;
-  prm.rows = static_cast<int64_t>(items.q0[items.n]) * a.num_q_heads;
-  prm.sl2 = a.scale * 1.4426950408889634f;
+  prm.sl2 = a.scale * kLog2e;
   prm.layer = a.layer;
-  prm.H = pool.num_kv_heads;
-  prm.G = a.num_q_heads / pool.num_kv_heads;
+  prm.H = H;
+  prm.gshift = G == 8 ? 3 : G == 4 ? 2 : G == 2 ? 1 : 0;
   prm.num_blocks = pool.num_blocks;
   prm.mbps = pool.mbps;
-  prm.bshift = pool.block_size == 32 ? 5 : 4;
-  prm.items = items;
-  const dim3 grid(static_cast<unsigned>((prm.rows + 7) / 8));
+  prm.bshift = pool.block_size == 32 ? 1 : 0;
+  prm.n = n;
+  prm.row0 = items.row0;
+  prm.part_rows = pair ? kTile : std::min(kTile, (max_rows + 7) / 8 * 8);
+
+  // KV tiles of a chunk: all of a sequence's, unless the units are too few for
+  // the SMs; then the smallest chunk that gives each SM one
+  auto count = [&](int chunk) {
+    int64_t u = 0;
+    for (int i = 0; i < n; ++i)
+      u += static_cast<int64_t>(ceil_div(items.q0[i + 1] - items.q0[i], ut)) *
+           ceil_div(ceil_div(items.kv_len[i], kTile), chunk);
+    return u * H;
+  };
+  int most = 1;
+  for (int i = 0; i < n; ++i) most = std::max(most, ceil_div(items.kv_len[i], kTile));
+  int chunk = most;
+  constexpr int kMinChunk = 4;
+  const int64_t room = pool.partial_slots * kPartialSlotFloats / (static_cast<int64_t>(prm.part_rows) * kPartFloats * kq);
+  const int64_t want = std::min<int64_t>(num_sms, room);
+  if (count(most) < want && most > kMinChunk) {
+    int lo = kMinChunk, hi = most;                // the smallest chunk with count <= want
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (count(mid) <= want) hi = mid; else lo = mid + 1;
+    }
+    chunk = lo;
+  }
+  prm.chunk = chunk;
+  const int64_t units = count(chunk);
+  if (units >= INT32_MAX / 4) return cudaErrorInvalidValue;
+  prm.units = static_cast<int32_t>(units);
+
+  // the longest sequences first
+  for (int i = 0; i < n; ++i) order[i] = i;
+  std::stable_sort(order, order + n, [&](int x, int y) { return items.kv_len[x] > items.kv_len[y]; });
+  prm.pre[0] = 0;
+  for (int k = 0; k < n; ++k) {
+    const int i = order[k];
+    prm.row[k] = items.row[i];
+    prm.kv_len[k] = items.kv_len[i];
+    prm.q0[k] = items.q0[i];
+    prm.m[k] = items.q0[i + 1] - items.q0[i];
+    prm.pre[k + 1] = prm.pre[k] + ceil_div(prm.m[k], ut) * ceil_div(ceil_div(prm.kv_len[k], kTile), chunk);
+  }
+
+  // q as [tokens][H_q][128], boxes of 128 / G tokens x G heads x 64
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(a.num_q_heads),
+                              static_cast<cuuint64_t>(a.total_tokens)};
+  const cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(a.num_q_heads) * kHeadDim * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tq)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUtensorMap tmq;
+  if (encode(&tmq, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(a.q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  cudaError_t e = pair ? dispatch<true>(pool, prm, maps, tmq, num_sms, stream)
+                       : dispatch<false>(pool, prm, maps, tmq, num_sms, stream);
+  if (e != cudaSuccess) return e;
   ++*launches;
-  if (pool.kv_dtype == kFP8)
-    return pool.act_dtype == kBF16 ? launch_pdl(attend_kernel<kFP8, kBF16>, grid, dim3(256), 0, stream, prm)
-                                   : launch_pdl(attend_kernel<kFP8, kFP16>, grid, dim3(256), 0, stream, prm);
-  return pool.act_dtype == kBF16 ? launch_pdl(attend_kernel<kBF16, kBF16>, grid, dim3(256), 0, stream, prm)
-                                 : launch_pdl(attend_kernel<kFP16, kFP16>, grid, dim3(256), 0, stream, prm);
+  if (chunk < most) {
+    const int tokens = items.q0[n];
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(tokens) * a.num_q_heads + 7) / 8));
+    e = pool.act_dtype == kBF16 ? launch_pdl(attend_merge_kernel<kBF16>, grid, dim3(256), 0, stream, prm, tokens, kq)
+                                : launch_pdl(attend_merge_kernel<kFP16>, grid, dim3(256), 0, stream, prm, tokens, kq);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace pa
