@@ -56,6 +56,13 @@ struct Ring {
   static constexpr int kStages = FP8 ? 3 : 5;
   static constexpr int kRawStages = FP8 ? (PAIR ? 4 : 5) : 0;
   static constexpr int kThreads = FP8 ? 512 : 384;
+  // Registers a thread: at launch (65,536 over the threads), then by role.  The
+  // softmax keeps a whole row of S; the shares add up to the launch's total.
+  static constexpr int kRegsLaunch = FP8 ? 128 : 168;
+  static constexpr int kRegsControl = FP8 ? 72 : 104;
+  static constexpr int kRegsSoftmax = FP8 ? 176 : 200;
+  static constexpr int kRegsConvert = FP8 ? 88 : 0;
+  static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsConvert <= kRegsLaunch * (kThreads / 128), "register shares");
   static constexpr int kOffKv = kQ * kOperand;
   static constexpr int kOffRaw = kOffKv + kStages * kOperand;
   static constexpr int kOffMeta = kOffRaw + kRawStages * kRaw;
@@ -170,21 +177,21 @@ __device__ __forceinline__ void tmem_wait(float (&v)[32]) {
                  "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]),
                  "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t a, const float (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
-      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
-      "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]),
-      "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]),
-      "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+// 16 columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t a, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(a)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -196,6 +203,35 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 template <int ACT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return ACT == kBF16 ? dev::pack_bf16(lo, hi) : dev::pack_f16(lo, hi);
+}
+
+// Two fp32 in one 64-bit register, and the packed operations on them.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_less() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Columns of a 32-column chunk whose first n are allowed.
@@ -217,7 +253,9 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
   Meta& mt = *reinterpret_cast<Meta*>(sm + R::kOffMeta);
   const uint32_t base = dev::smem_u32(sm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto bar = [](uint64_t& b) { return dev::smem_u32(&b); };
+  auto bar = [&](const uint64_t& b) {
+    return base + static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(&b) - sm);
+  };
   volatile int32_t* abort = &mt.abort;
   constexpr int kSchedConsumers = 1 + 8 + (kFp8 ? 4 : 0);  // warps that read a unit
 
@@ -260,7 +298,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
 
   // A warp's bounded wait, one outcome for all lanes; false ends the role.
   auto wait = [&](uint64_t& b, uint32_t parity) {
-    const uint32_t a = dev::smem_u32(&b);
+    const uint32_t a = bar(b);
     bool ok = false;
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
       if (dev::mbar_try_wait(a, parity)) {
@@ -287,6 +325,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     return u.seq_row >= 0;
   };
 
+  if (warp < 4) {
+  regs_less<R::kRegsControl>();
   if (warp == 0) {
     // ================================================================ producer
     uint32_t ring_i = 0, sched_i = 0, q_i[2] = {0, 0};
@@ -439,11 +479,12 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
       auto issue_s = [&](int x, int32_t i) {
         fence_after();
         if (lane == 0) {
-          const uint32_t qa = base + (PAIR ? x : 0) * kOperand, ka = stage(pos_k(i));
+          const uint64_t qd = smem_desc(base + (PAIR ? x : 0) * kOperand, 16, 1024);
+          const uint64_t kd = smem_desc(stage(pos_k(i)), 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-            mma_ss(tmem + x * 128, smem_desc(qa + o, 16, 1024), smem_desc(ka + o, 16, 1024), kIdS, kk > 0);
+            const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+            mma_ss(tmem + x * 128, qd + o, kd + o, kIdS, kk > 0);
           }
           commit(bar(mt.s_full[x]));
         }
@@ -452,11 +493,11 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
       auto issue_pv = [&](int x, int32_t i, bool acc) {
         fence_after();
         if (lane == 0) {
-          const uint32_t va = stage(pos_v(i));
+          const uint64_t vd = smem_desc(stage(pos_v(i)), kHalf, 1024);
           const int32_t steps = min(8, ((u.kv_len + 15) >> 4) - (u.tile0 + i) * 8);  // 16-token blocks copied
-          for (int j = 0; j < steps; ++j)
-            mma_ts(tmem + 256 + x * 128, tmem + x * 128 + j * 8, smem_desc(va + j * 2048, kHalf, 1024), kIdO,
-                   acc || j > 0);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < steps) mma_ts(tmem + 256 + x * 128, tmem + x * 128 + j * 8, vd + j * (2048 >> 4), kIdO, acc || j > 0);
         }
         __syncwarp();
       };
@@ -546,7 +587,9 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     if (lane == 0) commit(bar(mt.done));
     __syncwarp();
     dev::mbar_wait_bounded(bar(mt.done), 0, kWaitLimit);
-  } else if (warp >= 4 && warp < 12) {
+  }
+  } else if (warp < 12) {
+    regs_more<R::kRegsSoftmax>();
     // ======================================================= softmax, epilogue
     const int x = (warp >> 2) - 1;                     // stream
     const int r = (warp & 3) * 32 + lane;              // row, and TMEM lane
@@ -578,8 +621,9 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         sl2 *= prm.k_scale[prm.layer * prm.H + u.h];
         vs = prm.v_scale[prm.layer * prm.H + u.h];
       }
+      if (sl2 == 0.f) sl2 = 1e-30f;                     // equal weights; a masked -inf x sl2 stays -inf
       const bool neg = sl2 < 0.f;
-      const float asl2 = fabsf(sl2);
+      const float none = neg ? INFINITY : -INFINITY;    // a masked score: -inf once scaled
       float mref = -INFINITY, l = 0.f;
       bool ok = true;
       for (int32_t i = PAIR ? 0 : x; i < n; i += PAIR ? 1 : 2) {
@@ -589,37 +633,38 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         if (warp_ok) {
           const int32_t p0 = (u.tile0 + i) * kTile;
           const bool masked = p0 + kTile > lim_min;
-          // allowed columns of chunk c
-          auto allowed = [&](int c) {
-            const int32_t k = lim - (p0 + c * 32);
-            uint32_t a = low_bits(k);
-            if (prm.mask && k < 32) a |= k >= 0 ? static_cast<uint32_t>(bits << k) : (k > -64 ? static_cast<uint32_t>(bits >> -k) : 0u);
-            return a;
-          };
-          float v[2][32];
-          float mx = -INFINITY;
-          tmem_ld32(ts, v[0]);
+          // the whole row of S in registers; P overlays it as it is made
+          float y[4][32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_wait(v[c & 1]);
-            if (c < 3) tmem_ld32(ts + (c + 1) * 32, v[(c + 1) & 1]);
-            float(&y)[32] = v[c & 1];
-            if (masked) {
-              const uint32_t a = allowed(c);
+          for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, y[c]);
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (a >> k & 1) mx = fmaxf(mx, neg ? -y[k] : y[k]);
-            } else if (neg) {
+          for (int c = 0; c < 4; ++c) tmem_wait(y[c]);
+          if (masked) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, -y[k]);
-            } else {
+            for (int c = 0; c < 4; ++c) {
+              const int32_t k0 = lim - (p0 + c * 32);   // columns from the chunk's first to the limit
+              uint32_t a = low_bits(k0);
+              if (prm.mask && k0 < 32)
+                a |= k0 >= 0 ? static_cast<uint32_t>(bits << k0) : (k0 > -64 ? static_cast<uint32_t>(bits >> -k0) : 0u);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, y[k]);
+              for (int k = 0; k < 32; ++k) y[c][k] = a >> k & 1 ? y[c][k] : none;
             }
           }
-          mx *= asl2;      // -inf where nothing is allowed (NaN for a zero scale)
-          if (!(mx >= -3.0e38f)) mx = asl2 == 0.f ? 0.f : -INFINITY;
-          tmem_ld32(ts, v[0]);
+          float mc[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mc[k] = none;
+          if (neg) {
+#pragma unroll
+            for (int k = 0; k < 128; k += 2) mc[(k >> 1) & 7] = fminf(mc[(k >> 1) & 7], fminf(y[k >> 5][k & 31], y[k >> 5][(k & 31) + 1]));
+#pragma unroll
+            for (int k = 1; k < 8; ++k) mc[0] = fminf(mc[0], mc[k]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 128; k += 2) mc[(k >> 1) & 7] = fmaxf(mc[(k >> 1) & 7], fmaxf(y[k >> 5][k & 31], y[k >> 5][(k & 31) + 1]));
+#pragma unroll
+            for (int k = 1; k < 8; ++k) mc[0] = fmaxf(mc[0], mc[k]);
+          }
+          const float mx = mc[0] * sl2;      // -inf where nothing is allowed
           // the reference moves only when the maximum passes it by 2^8: O is
           // then scaled, after the P V of the step before (complete: S came after it)
           const bool move = mx > mref + kLazy || (mref == -INFINITY && mx > -INFINITY);
@@ -632,38 +677,34 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
           const bool first = i < (PAIR ? 1 : 2);
           if (!first && __any_sync(0xffffffffu, move)) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float o[32];
-              tmem_ld32(to + c * 32, o);
-              tmem_wait(o);
+            for (int c = 0; c < 8; ++c) {
+              float o[16];
+              tmem_ld16(to + c * 16, o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= corr;
-              tmem_st32(to + c * 32, o);
+              for (int k = 0; k < 16; ++k) o[k] *= corr;
+              tmem_st16(to + c * 16, reinterpret_cast<const uint32_t(&)[16]>(o));
             }
           }
-          const float mr = mref == -INFINITY ? 0.f : mref;
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          const float mr = mref == -INFINITY ? 0.f : -mref;
+          const uint64_t sl2x2 = pack_f32x2(sl2, sl2), mrx2 = pack_f32x2(mr, mr);
+          uint64_t ls[2] = {0, 0};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            tmem_wait(v[c & 1]);
-            if (c < 3) tmem_ld32(ts + (c + 1) * 32, v[(c + 1) & 1]);
-            float(&y)[32] = v[c & 1];
-            const uint32_t a = masked ? allowed(c) : 0xffffffffu;
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
-              float e0 = dev::exp2_approx(fmaf(y[k], sl2, -mr)), e1 = dev::exp2_approx(fmaf(y[k + 1], sl2, -mr));
-              if (masked) {
-                e0 = a >> k & 1 ? e0 : 0.f;
-                e1 = a >> (k + 1) & 1 ? e1 : 0.f;
-              }
-              ls[(k >> 1) & 3] += e0 + e1;
+              float e0, e1;
+              unpack_f32x2(fma_f32x2(pack_f32x2(y[c][k], y[c][k + 1]), sl2x2, mrx2), e0, e1);
+              e0 = dev::exp2_approx(e0);
+              e1 = dev::exp2_approx(e1);
+              ls[(k >> 1) & 1] = add_f32x2(ls[(k >> 1) & 1], pack_f32x2(e0, e1));
               pk[k >> 1] = pack2<ACT>(e0, e1);
             }
-            // P overlays S: chunk c goes to columns 16c .. 16c + 15, of S chunk c / 2
-            tmem_st16(ts + c * 16, pk);
+            tmem_st16(ts + c * 16, pk);      // columns of S chunk c / 2, which is in registers
           }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          float l0, l1;
+          unpack_f32x2(add_f32x2(ls[0], ls[1]), l0, l1);
+          l += l0 + l1;
           tmem_wait_st();
         }
         fence_before();
@@ -749,7 +790,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         if (!direct && row_ok && x == 0) *reinterpret_cast<float2*>(part + kHeadDim) = make_float2(mm, lsum);
       }
     }
-  } else if (kFp8 && warp >= 12) {
+  } else if constexpr (kFp8) {
+    regs_less<R::kRegsConvert>();
     // ================================================ FP8 codes to 16-bit tiles
     uint32_t raw_i = 0;
     const int tid = threadIdx.x - 384;
@@ -764,7 +806,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         const int32_t valid = min(kTile, u.kv_len - (u.tile0 + i) * kTile);
         const uint8_t* src = sm + R::kOffRaw + rs * kRaw;
         uint8_t* dst = sm + R::kOffKv + ks * kOperand;
-#pragma unroll
+#pragma unroll 2
         for (int k = 0; k < 8; ++k) {
           const int e = k * 128 + tid, tok = e >> 3, c = e & 7;      // 16 codes: 16c .. of token tok
           uint4 raw = *reinterpret_cast<const uint4*>(src + tok * 128 + ((c ^ (tok & 7)) << 4));
@@ -896,6 +938,11 @@ cudaError_t run(const Params& prm, const CacheMaps& maps, const CUtensorMap& tmq
     e = cudaFuncSetAttribute(attend_kernel<KV, ACT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem));
     if (e != cudaSuccess) return e;
+    // the warpgroups' register shares come out of what the launch holds
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, attend_kernel<KV, ACT, PAIR>);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs < R::kRegsLaunch) return cudaErrorInvalidConfiguration;
     if (dev < 64) configured |= uint64_t{1} << dev;
   }
   return launch_pdl(attend_kernel<KV, ACT, PAIR>, dim3(std::min(num_sms, prm.units)), dim3(R::kThreads), smem, stream,
