@@ -20,8 +20,8 @@
 //         KV read: prompts, wide trees);
 //   dual  both streams serve one query tile and take every other KV tile; their
 //         results are joined in the epilogue (few rows: bound by the KV read).
-// Roles: warp 0 claims work and issues the TMA copies (one box per 16-token
-// block and d-half), warp 1 issues the MMAs, warps 4-7 and 8-11 are the two
+// Roles: warp 0 claims work and loads queries, warps 0 and 2 issue the KV tiles'
+// TMA copies, warp 1 issues the MMAs, warp 3 zeroes V rows past a length, warps 4-7 and 8-11 are the two
 // softmax streams (a thread owns a row: its running maximum and sum need no
 // exchange), warps 12-15 convert FP8 codes to the activation type.
 // Work units are claimed from a counter, longest first.  Where there are too
@@ -45,6 +45,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 128;                      // rows of a query tile, positions of a KV tile
 constexpr int kHalf = kTile * 128;              // one 64-element d-half of a 16-bit tile (16 KB)
 constexpr int kOperand = 2 * kHalf;             // a 16-bit tile (32 KB)
+constexpr int kLoaders = 2;                     // warps that issue a tile's copies, 8 / kLoaders blocks each
 constexpr int kRaw = kTile * 128;               // an FP8 tile (16 KB)
 constexpr int kPartFloats = kHeadDim + 2;       // of one row: O, maximum, sum
 constexpr float kLazy = 8.f;                    // log2 units a row's maximum may pass its reference by
@@ -84,11 +85,11 @@ struct Unit {
 struct Meta {
   uint64_t kv_full[6], kv_empty[6], raw_full[6], raw_empty[6];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], ml[2];
-  uint64_t sched_full[2], sched_empty[2], done;
+  uint64_t sched_full[2], sched_empty[2], done, clean_go, clean_done;
   Unit unit[2];
   uint32_t tmem;
   int32_t abort;
-  int32_t rows[8][8];     // cache rows of the last 8 tiles' blocks
+  int32_t rows[kLoaders][8][8 / kLoaders];  // cache rows of the last 8 tiles' blocks
   float mlv[2][2][2][kTile];  // [unit parity][stream][max, sum][row] (dual)
 };
 
@@ -257,13 +258,13 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     return base + static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(&b) - sm);
   };
   volatile int32_t* abort = &mt.abort;
-  constexpr int kSchedConsumers = 1 + 8 + (kFp8 ? 4 : 0);  // warps that read a unit
+  constexpr int kSchedConsumers = kLoaders + 8 + (kFp8 ? 4 : 1);  // warps that read a unit
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 6; ++s) {
-      dev::mbar_init(bar(mt.kv_full[s]), kFp8 ? 4 : 1);
+      dev::mbar_init(bar(mt.kv_full[s]), kFp8 ? 4 : kLoaders);
       dev::mbar_init(bar(mt.kv_empty[s]), 1);
-      dev::mbar_init(bar(mt.raw_full[s]), 1);
+      dev::mbar_init(bar(mt.raw_full[s]), kLoaders);
       dev::mbar_init(bar(mt.raw_empty[s]), 4);
     }
     for (int x = 0; x < 2; ++x) {
@@ -278,6 +279,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
       dev::mbar_init(bar(mt.sched_empty[x]), kSchedConsumers);
     }
     dev::mbar_init(bar(mt.done), 1);
+    dev::mbar_init(bar(mt.clean_go), 1);
+    dev::mbar_init(bar(mt.clean_done), 1);
     mt.abort = 0;
     dev::fence_mbar_init();
     dev::tma_prefetch_desc(&tmk);
@@ -325,11 +328,89 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     return u.seq_row >= 0;
   };
 
+  // 16-bit tiles: the unit's last KV tile ends inside a block.
+  auto needs_clean = [](const Unit& u, int32_t n) {
+    const int32_t valid = u.kv_len - (u.tile0 + n - 1) * kTile;
+    return !kFp8 && valid < kTile && (valid & 15);
+  };
+
+  // ------------------------------------------------------------------ loaders
+  // KV tiles in ring order: K(0 .. kLead-1), then V(i), K(i + kLead), ...  One
+  // warp gets a copy out every ~60 ns (a lane at a time), so kLoaders warps share
+  // each tile's blocks.  16-bit tiles: K as two boxes a block, [2 d-halves][128]
+  // [128 B] (the rows of a d-half must be evenly spaced for the MMA); V, whose
+  // MMA takes one 16-token block a step, as one box of both d-halves a block.
+  constexpr uint32_t kDepth = kFp8 ? R::kRawStages : R::kStages;
+  constexpr int kShare = 8 / kLoaders;
+  uint32_t ring_i = 0;
+  auto load_unit = [&](const Unit& u) {
+    const int part = warp >> 1;                                      // warps 0, 2
+    const int32_t n = max(u.n0, u.n1);
+    const int32_t* table = prm.tables + static_cast<int64_t>(u.seq_row) * prm.mbps;
+    const int32_t blocks = (u.kv_len + 15) >> 4;                     // of 16 tokens
+    int32_t id = 0, id_base = -64;
+    auto copy = [&](int32_t i, bool is_v) {
+      const int32_t b0 = (u.tile0 + i) * 8, nb = max(0, min(kShare, blocks - b0 - part * kShare));
+      if (!is_v) {  // the tile's cache rows, kept for its V copy
+        if (b0 >= id_base + 32 || id_base < 0) {
+          id_base = b0;
+          const int32_t b = b0 + lane, e = b >> prm.bshift;
+          int32_t v = b < blocks && e < prm.mbps ? table[e] : 0;
+          if (static_cast<uint32_t>(v) >= static_cast<uint32_t>(prm.num_blocks)) {
+            atomicOr(prm.err, kErrBadBlock);
+            v = 0;
+          }
+          id = (((prm.layer * prm.num_blocks + v) * prm.H + u.h) << (4 + prm.bshift)) +
+               (b & ((1 << prm.bshift) - 1)) * 16;
+        }
+        const int32_t row = __shfl_sync(0xffffffffu, id, (b0 - id_base + part * kShare + lane) & 31);
+        if (lane < kShare) mt.rows[part][i & 7][lane] = row;
+        __syncwarp();
+      }
+      const uint32_t st = ring_i % kDepth, par = ((ring_i / kDepth) & 1) ^ 1;
+      if (!wait(kFp8 ? mt.raw_empty[st] : mt.kv_empty[st], par)) return false;
+      const uint32_t full = bar(kFp8 ? mt.raw_full[st] : mt.kv_full[st]);
+      if (lane == 0) dev::mbar_arrive_expect_tx(full, nb * (kFp8 ? 2048 : 4096));
+      __syncwarp();  // the bytes are expected before any copy is issued
+      const int j = lane % kShare, half = lane / kShare;
+      const uint32_t dst = base + (kFp8 ? R::kOffRaw + st * kRaw : R::kOffKv + st * kOperand);
+      if (j < nb) {
+        const int32_t row = mt.rows[part][i & 7][j], jb = part * kShare + j;
+        if (kFp8) {
+          if (half == 0) dev::tma_load_2d(dst + jb * 2048, is_v ? &tmv : &tmk, 0, row, full);
+        } else if (is_v) {
+          if (half == 0) dev::tma_load_3d(dst + jb * 4096, &tmv, 0, row, 0, full);
+        } else if (half < 2) {
+          dev::tma_load_2d(dst + half * kHalf + jb * 2048, &tmk, half * 64, row, full);
+        }
+      }
+      ++ring_i;
+      return true;
+    };
+    for (int32_t i = 0; i < min(kLead, n); ++i)
+      if (!copy(i, false)) return false;
+    for (int32_t i = 0; i < n; ++i) {
+      if (!copy(i, true)) return false;
+      if (i + kLead < n && !copy(i + kLead, false)) return false;
+    }
+    return true;
+  };
+  // copies already issued land before the CTA can exit
+  auto load_drain = [&]() {
+    for (uint32_t k = ring_i > kDepth ? ring_i - kDepth : 0; k < ring_i; ++k)
+      dev::mbar_wait_bounded(bar(kFp8 ? mt.raw_full[k % kDepth] : mt.kv_full[k % kDepth]), (k / kDepth) & 1, kWaitLimit);
+  };
+
   if (warp < 4) {
   regs_less<R::kRegsControl>();
-  if (warp == 0) {
-    // ================================================================ producer
-    uint32_t ring_i = 0, sched_i = 0, q_i[2] = {0, 0};
+  if (warp == 2) {
+    Unit u;
+    while (next_unit(u) && load_unit(u)) {
+    }
+    load_drain();
+  } else if (warp == 0) {
+    // ===================================== schedule, queries, and a loader
+    uint32_t sched_i = 0, q_i[2] = {0, 0};
     int32_t w = blockIdx.x, w_next = 0;
     bool ok = true;
     const int32_t total = prm.units;
@@ -343,7 +424,6 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
       }
       Unit u;
       u.seq_row = -1;
-      const int32_t* table = prm.tables;
       if (w < total) {
         const int32_t wi = w / prm.H;
         u.h = w - wi * prm.H;
@@ -376,7 +456,6 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         }
         u.n0 = nx[0];
         u.n1 = nx[1];
-        table += static_cast<int64_t>(u.seq_row) * prm.mbps;
       }
       const int32_t n = u.seq_row < 0 ? 0 : max(u.n0, u.n1);
       if (u.seq_row < 0 || n > 0) {                                  // an empty chunk is skipped
@@ -403,190 +482,171 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
           ++q_i[x];
         }
         if (!ok) break;
-        // KV tiles: K(0..kLead-1), then V(i), K(i + kLead), ...
-        const int32_t blocks = (u.kv_len + 15) >> 4;                 // of 16 tokens
-        int32_t id = 0;
-        int32_t id_base = -64;
-        auto copy = [&](int32_t i, bool is_v) {
-          const int32_t b0 = (u.tile0 + i) * 8, nb = min(8, blocks - b0);
-          if (!is_v) {  // the tile's cache rows, kept for its V copy
-            if (b0 >= id_base + 32 || id_base < 0) {
-              id_base = b0;
-              const int32_t b = b0 + lane, e = b >> prm.bshift;
-              int32_t v = b < blocks && e < prm.mbps ? table[e] : 0;
-              if (static_cast<uint32_t>(v) >= static_cast<uint32_t>(prm.num_blocks)) {
-                atomicOr(prm.err, kErrBadBlock);
-                v = 0;
-              }
-              id = (((prm.layer * prm.num_blocks + v) * prm.H + u.h) << (4 + prm.bshift)) +
-                   (b & ((1 << prm.bshift) - 1)) * 16;
-            }
-            const int32_t row = __shfl_sync(0xffffffffu, id, (b0 - id_base + lane) & 31);
-            if (lane < 8) mt.rows[i & 7][lane] = row;
-            __syncwarp();
-          }
-          const CUtensorMap* map = is_v ? &tmv : &tmk;
-          constexpr int kDepth = kFp8 ? R::kRawStages : R::kStages;
-          const uint32_t st = ring_i % kDepth, par = ((ring_i / kDepth) & 1) ^ 1;
-          if (!wait(kFp8 ? mt.raw_empty[st] : mt.kv_empty[st], par)) return false;
-          const uint32_t full = bar(kFp8 ? mt.raw_full[st] : mt.kv_full[st]);
-          if (lane == 0) dev::mbar_arrive_expect_tx(full, nb * (kFp8 ? 2048 : 4096));
-          __syncwarp();  // the bytes are expected before any copy is issued
-          const int j = lane & 7, half = lane >> 3;
-          if (j < nb && half < (kFp8 ? 1 : 2)) {
-            const uint32_t dst = base + (kFp8 ? R::kOffRaw + st * kRaw : R::kOffKv + st * kOperand) + half * kHalf + j * 2048;
-            dev::tma_load_2d(dst, map, half * 64, mt.rows[i & 7][j], full);
-          }
-          ++ring_i;
-          return true;
-        };
-        for (int32_t i = 0; ok && i < min(kLead, n); ++i) ok = copy(i, false);
-        for (int32_t i = 0; ok && i < n; ++i) {
-          ok = copy(i, true);
-          if (ok && i + kLead < n) ok = copy(i + kLead, false);
-        }
-        if (!ok) break;
+        if (!(ok = load_unit(u))) break;
       }
       w = __shfl_sync(0xffffffffu, w_next, 0);
     }
     dev::grid_dep_launch();
-    // copies already issued land before the CTA can exit
-    constexpr uint32_t kDepth = kFp8 ? R::kRawStages : R::kStages;
-    for (uint32_t k = ring_i > kDepth ? ring_i - kDepth : 0; k < ring_i; ++k)
-      dev::mbar_wait_bounded(bar(kFp8 ? mt.raw_full[k % kDepth] : mt.kv_full[k % kDepth]), (k / kDepth) & 1, kWaitLimit);
+    load_drain();
     for (int x = 0; x < R::kQ; ++x)
       if (q_i[x]) dev::mbar_wait_bounded(bar(mt.q_full[x]), (q_i[x] - 1) & 1, kWaitLimit);
   } else if (warp == 1) {
     // ===================================================================== MMA
-    constexpr bool kBf = ACT == kBF16;
-    constexpr uint32_t kIdS = instr_desc(kBf, false), kIdO = instr_desc(kBf, true);
-    uint32_t kv_i = 0, q_i[2] = {0, 0}, p_i[2] = {0, 0}, o_i[2] = {0, 0};
-    Unit u;
-    bool ok = true;
-    while (ok && next_unit(u)) {
-      const int32_t n = max(u.n0, u.n1);
-      // ring positions of the unit's K and V tiles
-      auto pos_k = [&](int32_t i) { return PAIR ? 2 * i : (i == 0 ? 0 : 2 * i - 1); };
-      auto pos_v = [&](int32_t i) { return PAIR ? 2 * i + 1 : (i == n - 1 ? 2 * n - 1 : 2 * i + 2); };
-      auto kv_wait = [&](int32_t pos) {
-        const uint32_t k = kv_i + pos;
-        return wait(mt.kv_full[k % R::kStages], (k / R::kStages) & 1);
-      };
-      auto kv_release = [&](int32_t pos) {
-        if (lane == 0) commit(bar(mt.kv_empty[(kv_i + pos) % R::kStages]));
-      };
-      auto stage = [&](int32_t pos) { return base + R::kOffKv + ((kv_i + pos) % R::kStages) * kOperand; };
-      auto issue_s = [&](int x, int32_t i) {
-        fence_after();
-        if (lane == 0) {
-          const uint64_t qd = smem_desc(base + (PAIR ? x : 0) * kOperand, 16, 1024);
-          const uint64_t kd = smem_desc(stage(pos_k(i)), 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-            mma_ss(tmem + x * 128, qd + o, kd + o, kIdS, kk > 0);
-          }
-          commit(bar(mt.s_full[x]));
+    // One thread runs the whole role: what it does between two MMAs is time the
+    // tensor core may stand still.
+    if (dev::elect_one()) {
+      constexpr bool kBf = ACT == kBF16;
+      constexpr uint32_t kIdS = instr_desc(kBf, false), kIdO = instr_desc(kBf, true);
+      const uint64_t q_desc = smem_desc(base, 16, 1024), k_desc = smem_desc(base + R::kOffKv, 16, 1024),
+                     v_desc = smem_desc(base + R::kOffKv, 2048, 1024);
+      uint32_t st = 0, ph = 0;                          // ring stage of the next tile, and its phase
+      uint32_t q_i[2] = {0, 0}, p_i[2] = {0, 0}, o_i[2] = {0, 0}, clean_i = 0;
+      bool ok = true;
+      auto wait1 = [&](uint64_t& b, uint32_t parity) {
+        const uint32_t a = bar(b);
+        for (uint32_t i = 0; i < kWaitLimit; ++i) {
+          if (dev::mbar_try_wait(a, parity)) return true;
+          if (*abort) break;
         }
-        __syncwarp();
+        if (*abort == 0) {
+          *abort = 1;
+          atomicOr(prm.err, kErrTimeout);
+        }
+        return ok = false;
       };
-      auto issue_pv = [&](int x, int32_t i, bool acc) {
+      auto advance = [&]() {                            // to the next tile of the ring, which has landed
+        const uint32_t s = st;
+        if (++st == R::kStages) {
+          st = 0;
+          ph ^= 1;
+        }
+        return s;
+      };
+      auto issue_s = [&](int x, uint32_t s) {
         fence_after();
-        if (lane == 0) {
-          const uint64_t vd = smem_desc(stage(pos_v(i)), kHalf, 1024);
-          const int32_t steps = min(8, ((u.kv_len + 15) >> 4) - (u.tile0 + i) * 8);  // 16-token blocks copied
+        const uint64_t qd = q_desc + (PAIR ? x : 0) * (kOperand >> 4), kd = k_desc + s * (kOperand >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + x * 128, qd + o, kd + o, kIdS, kk > 0);
+        }
+        commit(bar(mt.s_full[x]));
+      };
+      auto issue_pv = [&](int x, uint32_t s, int32_t steps, bool acc) {   // steps: 16-token blocks copied
+        fence_after();
+        const uint64_t vd = v_desc + s * (kOperand >> 4);
+        if (steps >= 8) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (j < steps) mma_ts(tmem + 256 + x * 128, tmem + x * 128 + j * 8, vd + j * (2048 >> 4), kIdO, acc || j > 0);
+            mma_ts(tmem + 256 + x * 128, tmem + x * 128 + j * 8, vd + j * (4096 >> 4), kIdO, acc || j > 0);
+        } else {
+          for (int j = 0; j < steps; ++j)
+            mma_ts(tmem + 256 + x * 128, tmem + x * 128 + j * 8, vd + j * (4096 >> 4), kIdO, acc || j > 0);
         }
-        __syncwarp();
       };
-      // V rows past the length: their weights are 0, and 0 x NaN is NaN
-      auto clean_v = [&](int32_t i) {
-        if constexpr (!kFp8) {
-          const int32_t valid = u.kv_len - (u.tile0 + i) * kTile;
-          if (valid < kTile && (valid & 15)) {
-            uint8_t* v = sm + (stage(pos_v(i)) - base);
-            const int32_t rows = 16 - (valid & 15);
-            for (int c = lane; c < rows * 16; c += 32)
-              *reinterpret_cast<uint4*>(v + (c & 1) * kHalf + (valid + (c >> 4)) * 128 + ((c >> 1) & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            dev::fence_proxy_async_smem();
-            __syncwarp();
+      for (;;) {
+        if (!wait1(mt.sched_full[unit_i & 1], (unit_i >> 1) & 1)) break;
+        const Unit& un = mt.unit[unit_i & 1];
+        const int32_t seq_row = un.seq_row, n0 = un.n0, n1 = un.n1, n = max(n0, n1);
+        const int32_t blocks = ((un.kv_len + 15) >> 4) - un.tile0 * 8;    // 16-token blocks from the first tile on
+        const bool clean = needs_clean(un, n);
+        arrive(bar(mt.sched_empty[unit_i & 1]));
+        ++unit_i;
+        if (seq_row < 0) break;
+        // V of tile i: landed, and its rows past the length zeroed
+        auto take_v = [&](int32_t i) {
+          if (!wait1(mt.kv_full[st], ph)) return st;
+          if (clean && i == n - 1) {
+            arrive(bar(mt.clean_go));
+            wait1(mt.clean_done, clean_i & 1);
+            ++clean_i;
           }
-        }
-      };
-      if constexpr (PAIR) {
-        const int32_t nx[2] = {u.n0, u.n1};
-        if (!(ok = kv_wait(pos_k(0)))) break;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok || nx[x] == 0) continue;
-          if (!(ok = wait(mt.q_full[x], q_i[x] & 1))) break;
-          ++q_i[x];
-          issue_s(x, 0);
-          if (nx[x] == 1 && lane == 0) commit(bar(mt.q_empty[x]));
-        }
-        if (!ok) break;
-        kv_release(pos_k(0));
-        for (int32_t j = 0; ok && j < n; ++j) {
-          if (!(ok = kv_wait(pos_v(j)))) break;
-          clean_v(j);
-          if (j + 1 < n && !(ok = kv_wait(pos_k(j + 1)))) break;
+          return advance();
+        };
+        auto take_k = [&]() { return wait1(mt.kv_full[st], ph) ? advance() : st; };
+        if constexpr (PAIR) {
+          const int32_t nx[2] = {n0, n1};
+          const uint32_t k0 = take_k();
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (!ok || j >= nx[x]) continue;
-            if (j == 0) {
-              if (!(ok = wait(mt.o_free[x], (o_i[x] & 1) ^ 1))) break;
-              ++o_i[x];
-            }
-            if (!(ok = wait(mt.p_full[x], p_i[x] & 1))) break;
-            ++p_i[x];
-            issue_pv(x, j, j > 0);
-            if (j == nx[x] - 1 && lane == 0) commit(bar(mt.o_full[x]));
-            if (x == 1 || j >= nx[1]) kv_release(pos_v(j));
-            if (j + 1 < nx[x]) {
-              issue_s(x, j + 1);
-              if (j + 1 == nx[x] - 1 && lane == 0) commit(bar(mt.q_empty[x]));
-            }
-            if (j + 1 < n && (x == 1 || j >= nx[1])) kv_release(pos_k(j + 1));
+            if (!ok || nx[x] == 0 || !wait1(mt.q_full[x], q_i[x] & 1)) continue;
+            ++q_i[x];
+            issue_s(x, k0);
+            if (nx[x] == 1) commit(bar(mt.q_empty[x]));
           }
-        }
-      } else {
-        if (!(ok = wait(mt.q_full[0], q_i[0] & 1))) break;
-        ++q_i[0];
-        for (int32_t i = 0; ok && i < min(2, n); ++i) {
-          if (!(ok = kv_wait(pos_k(i)))) break;
-          issue_s(i, i);
-          kv_release(pos_k(i));
-          if (i == n - 1 && lane == 0) commit(bar(mt.q_empty[0]));
+          if (!ok) break;
+          commit(bar(mt.kv_empty[k0]));
+          for (int32_t j = 0; ok && j < n; ++j) {
+            const uint32_t v = take_v(j), k = j + 1 < n ? take_k() : 0;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (!ok || j >= nx[x]) continue;
+              if (j == 0 && !wait1(mt.o_free[x], (o_i[x]++ & 1) ^ 1)) continue;
+              if (!wait1(mt.p_full[x], p_i[x] & 1)) continue;
+              ++p_i[x];
+              issue_pv(x, v, blocks - j * 8, j > 0);
+              if (x == 1 || j >= nx[1]) commit(bar(mt.kv_empty[v]));
+              if (j == nx[x] - 1) commit(bar(mt.o_full[x]));
+              if (j + 1 < nx[x]) {
+                issue_s(x, k);
+                if (j + 1 == nx[x] - 1) commit(bar(mt.q_empty[x]));
+              }
+              if (j + 1 < n && (x == 1 || j >= nx[1])) commit(bar(mt.kv_empty[k]));
+            }
+          }
+        } else {
+          if (!wait1(mt.q_full[0], q_i[0] & 1)) break;
+          ++q_i[0];
+          for (int32_t i = 0; ok && i < min(2, n); ++i) {
+            const uint32_t k = take_k();
+            if (!ok) break;
+            issue_s(i, k);
+            commit(bar(mt.kv_empty[k]));
+            if (i == n - 1) commit(bar(mt.q_empty[0]));
+          }
+          if (!ok || !wait1(mt.o_free[0], (o_i[0]++ & 1) ^ 1)) break;
+          for (int32_t i = 0; i < n; ++i) {
+            const int x = i & 1;
+            const uint32_t v = take_v(i);
+            if (!ok || !wait1(mt.p_full[x], p_i[x]++ & 1)) break;
+            issue_pv(x, v, blocks - i * 8, i > 1);
+            commit(bar(mt.kv_empty[v]));
+            if (i >= n - 2) commit(bar(mt.o_full[x]));
+            if (i + 2 < n) {
+              const uint32_t k = take_k();
+              if (!ok) break;
+              issue_s(x, k);
+              commit(bar(mt.kv_empty[k]));
+              if (i + 2 == n - 1) commit(bar(mt.q_empty[0]));
+            }
+          }
         }
         if (!ok) break;
-        if (!(ok = wait(mt.o_free[0], (o_i[0] & 1) ^ 1))) break;
-        ++o_i[0];
-        for (int32_t i = 0; i < n; ++i) {
-          const int x = i & 1;
-          if (!(ok = kv_wait(pos_v(i)))) break;
-          clean_v(i);
-          if (!(ok = wait(mt.p_full[x], p_i[x] & 1))) break;
-          ++p_i[x];
-          issue_pv(x, i, i > 1);
-          kv_release(pos_v(i));
-          if (i >= n - 2 && lane == 0) commit(bar(mt.o_full[x]));
-          if (i + 2 < n) {
-            if (!(ok = kv_wait(pos_k(i + 2)))) break;
-            issue_s(x, i + 2);
-            kv_release(pos_k(i + 2));
-            if (i + 2 == n - 1 && lane == 0) commit(bar(mt.q_empty[0]));
-          }
-        }
       }
-      kv_i += 2 * n;
+      // every MMA issued has finished before the tensor memory is released
+      commit(bar(mt.done));
+      dev::mbar_wait_bounded(bar(mt.done), 0, kWaitLimit);
     }
-    // every MMA issued has finished before the tensor memory is released
-    if (lane == 0) commit(bar(mt.done));
     __syncwarp();
-    dev::mbar_wait_bounded(bar(mt.done), 0, kWaitLimit);
+  } else if (!kFp8) {
+    // ============================================== V rows past the length
+    // Their weights are 0, and 0 x NaN is NaN: zeroed where a block is partly filled.
+    uint32_t kv_i = 0, clean_i = 0;
+    Unit u;
+    while (next_unit(u)) {
+      const int32_t n = max(u.n0, u.n1);
+      kv_i += 2 * n;                                    // the last V is the unit's last tile in the ring
+      if (!needs_clean(u, n)) continue;
+      if (!wait(mt.clean_go, clean_i & 1)) break;
+      ++clean_i;
+      const int32_t valid = u.kv_len - (u.tile0 + n - 1) * kTile;
+      uint8_t* v = sm + R::kOffKv + ((kv_i - 1) % R::kStages) * kOperand + (valid >> 4) * 4096 + (valid & 15) * 128;
+      for (int c = lane; c < (16 - (valid & 15)) * 16; c += 32)
+        *reinterpret_cast<uint4*>(v + (c & 1) * 2048 + (c >> 4) * 128 + ((c >> 1) & 7) * 16) = make_uint4(0, 0, 0, 0);
+      dev::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive(bar(mt.clean_done));
+    }
   }
   } else if (warp < 12) {
     regs_more<R::kRegsSoftmax>();
@@ -818,7 +878,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
             const uint32_t h2 = dev::e4m3x2_to_f16x2(static_cast<uint16_t>(wsrc[q >> 1] >> ((q & 1) * 16)));
             o[q] = ACT == kBF16 ? dev::pack_bf16(dev::f16lo_to_f32(h2), dev::f16hi_to_f32(h2)) : h2;
           }
-          uint8_t* row = dst + (c >> 2) * kHalf + tok * 128;
+          uint8_t* row = is_v ? dst + (tok >> 4) * 4096 + (c >> 2) * 2048 + (tok & 15) * 128
+                              : dst + (c >> 2) * kHalf + tok * 128;
           const int cc = 2 * (c & 3), sw = tok & 7;
           // the two d-halves write their chunks in opposite order: no bank is hit twice
           const int f = c >> 2;
@@ -946,7 +1007,7 @@ cudaError_t run(const Params& prm, const CacheMaps& maps, const CUtensorMap& tmq
     if (dev < 64) configured |= uint64_t{1} << dev;
   }
   return launch_pdl(attend_kernel<KV, ACT, PAIR>, dim3(std::min(num_sms, prm.units)), dim3(R::kThreads), smem, stream,
-                    prm, maps.k, maps.v, tmq);
+                    prm, maps.k, maps.v3, tmq);
 }
 
 template <bool PAIR>
