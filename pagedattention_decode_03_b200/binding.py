@@ -7,6 +7,7 @@ If the shared library has not been built, the first call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from dataclasses import dataclass, field
@@ -206,6 +207,8 @@ class Pool:
     v_cache: object = None
     workspace: object = None
     scales: tuple = ()
+    device: int = -1          # CUDA ordinal; -1: host-only pool
+    _types: object = None
     _keep: list = field(default_factory=list)
 
     def __del__(self):
@@ -269,7 +272,8 @@ def pa_pool_create(*, num_layers: int, num_kv_heads: int, block_size: int, num_b
                 block_size=block_size, num_blocks=num_blocks, max_seqs=max_seqs,
                 max_blocks_per_seq=max_blocks_per_seq, kv_dtype=kv_dtype, act_dtype=act_dtype,
                 k_cache=k_cache, v_cache=v_cache, workspace=workspace,
-                scales=(k_scale, v_scale, k_inv_scale, v_inv_scale), _keep=keep)
+                scales=(k_scale, v_scale, k_inv_scale, v_inv_scale), device=-1 if host_only else d.device,
+                _keep=keep)
 
 
 def pa_pool_destroy(pool: Pool) -> None:
@@ -400,29 +404,57 @@ def pa_decode_attention_noalloc(desc: pa_pool_desc, layer: int, block_tables, se
            "pa_decode_attention_noalloc")
 
 
-def _pool_stream(pool: Pool, stream):
-    """`stream`, or the pool's device's current one."""
-    if stream is not None:
-        return _stream(stream)
+def _pool_stream(pool: Pool, stream) -> int:
+    """Handle of `stream`, or of the pool's device's current one."""
+    if stream is None:
+        return _current_stream(pool.device) if pool.device >= 0 else 0
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _current_stream(device: int) -> int:
+    # the raw handle without a Stream object, where this torch has it
+    global _current_stream
     import torch
-    if not torch.cuda.is_available():
-        return ctypes.c_void_p(0)
-    return ctypes.c_void_p(torch.cuda.current_stream(pool.desc.device).cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _current_stream = raw or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _current_stream(device)
 
 
 def _pool_tensor(pool: Pool, t, name: str, dtype, shape) -> int:
-    """Address of a contiguous tensor of this type and shape on the pool's device
-    (None in `shape`: any size there)."""
-    if not t.is_cuda or t.device.index != pool.desc.device or not t.is_contiguous() or t.dtype != dtype:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{pool.desc.device}")
-    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+    """Address of a contiguous tensor of this type and shape on the pool's device."""
+    if t.get_device() != pool.device or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{pool.device}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _act(pool: Pool):
-    import torch
-    return torch.bfloat16 if pool.act_dtype == "bf16" else torch.float16
+def _device_pool(pool: Pool):
+    """The pool's activation type and int32, as torch has them."""
+    if pool.device < 0:
+        raise ValueError("host-only pool: no device buffers")
+    if pool._types is None:
+        import torch
+        pool._types = (torch.bfloat16 if pool.act_dtype == "bf16" else torch.float16, torch.int32)
+    return pool._types
+
+
+def _ints(xs):
+    """Host int32 values with a buffer address: (address, count, owner)."""
+    if isinstance(xs, (list, tuple)):
+        try:
+            a = array.array("i", xs)
+            return a.buffer_info()[0], len(a), a
+        except TypeError:
+            pass
+    a = _i32(xs)
+    return a.ctypes.data, len(a), a
+
+
+def _len1(t, name: str) -> int:
+    if t.dim() != 1:
+        raise ValueError(f"{name} must have one dimension, got shape {tuple(t.shape)}")
+    return t.shape[0]
 
 
 def pa_build_tables(pool: Pool, old_lens, new_lens, free_blocks, free_head, free_head_out, block_tables,
@@ -431,57 +463,55 @@ def pa_build_tables(pool: Pool, old_lens, new_lens, free_blocks, free_head, free
     tokens' slots, on the GPU.  All arguments are int32 device tensors: lengths [n],
     free_blocks [F], free_head / free_head_out [1], block_tables [n][max_blocks_per_seq],
     cu_tokens [n + 1], slots [capacity]."""
-    import torch
-    n = old_lens.shape[0] if old_lens.dim() == 1 else -1
-    i32 = torch.int32
-    ptrs = [_pool_tensor(pool, t, name, i32, shape) for t, name, shape in (
-        (old_lens, "old_lens", (n,)), (new_lens, "new_lens", (n,)), (free_blocks, "free_blocks", (None,)),
-        (free_head, "free_head", (1,)), (free_head_out, "free_head_out", (1,)),
-        (block_tables, "block_tables", (n, pool.max_blocks_per_seq)), (cu_tokens, "cu_tokens", (n + 1,)),
-        (slots, "slots", (None,)))]
-    old, new, free, head, head_out, tab, cu, sl = ptrs
-    _check(lib().pa_build_tables(pool.handle, n, old, new, free, free_blocks.shape[0], head, head_out, tab, cu,
-                                 sl, slots.shape[0], _pool_stream(pool, stream)), "pa_build_tables")
+    i32 = _device_pool(pool)[1]
+    n, F, cap = _len1(old_lens, "old_lens"), _len1(free_blocks, "free_blocks"), _len1(slots, "slots")
+    st = lib().pa_build_tables(
+        pool.handle, n, _pool_tensor(pool, old_lens, "old_lens", i32, (n,)),
+        _pool_tensor(pool, new_lens, "new_lens", i32, (n,)),
+        _pool_tensor(pool, free_blocks, "free_blocks", i32, (F,)), F,
+        _pool_tensor(pool, free_head, "free_head", i32, (1,)),
+        _pool_tensor(pool, free_head_out, "free_head_out", i32, (1,)),
+        _pool_tensor(pool, block_tables, "block_tables", i32, (n, pool.max_blocks_per_seq)),
+        _pool_tensor(pool, cu_tokens, "cu_tokens", i32, (n + 1,)),
+        _pool_tensor(pool, slots, "slots", i32, (cap,)), cap, _pool_stream(pool, stream))
+    if st != PA_OK:
+        _check(st, "pa_build_tables")
 
 
 def pa_append_kv_slots(pool: Pool, layer: int, slots, k_new, v_new, stream=None) -> None:
     """Write row t of k_new / v_new [T][H_kv][128] to cache slot slots[t] (int32 device
     tensor [T]; -1 skips the row) of `layer`."""
-    import torch
-    T = slots.shape[0] if slots.dim() == 1 else -1
+    act, i32 = _device_pool(pool)
+    T = _len1(slots, "slots")
     shape = (T, pool.num_kv_heads, 128)
-    sp = _pool_tensor(pool, slots, "slots", torch.int32, (T,))
-    kp = _pool_tensor(pool, k_new, "k_new", _act(pool), shape)
-    vp = _pool_tensor(pool, v_new, "v_new", _act(pool), shape)
-    _check(lib().pa_append_kv_slots(pool.handle, layer, T, sp, kp, vp, _pool_stream(pool, stream)),
-           "pa_append_kv_slots")
+    st = lib().pa_append_kv_slots(pool.handle, layer, T, _pool_tensor(pool, slots, "slots", i32, (T,)),
+                                  _pool_tensor(pool, k_new, "k_new", act, shape),
+                                  _pool_tensor(pool, v_new, "v_new", act, shape), _pool_stream(pool, stream))
+    if st != PA_OK:
+        _check(st, "pa_append_kv_slots")
 
 
-def _attend(fn, where: str, pool: Pool, layer: int, lens, mask, q, out, scale: float, seqs, kv_lens,
-            block_tables, stream) -> None:
-    import torch
-    m = _i32(lens)
-    n = len(m)
-    rows = int(m.sum(dtype=np.int64))
+def _attend_args(pool: Pool, lens, q, out, seqs, kv_lens, block_tables):
+    """Addresses and sizes of the arguments both attentions share; the last entry
+    keeps the host arrays alive."""
+    act, i32 = _device_pool(pool)
+    m, n, keep = _ints(lens)
+    rows = sum(keep) if isinstance(keep, array.array) else int(keep.sum(dtype=np.int64))
     hq = q.shape[1] if q.dim() == 3 else -1
-    qp = _pool_tensor(pool, q, "q", _act(pool), (rows, hq, 128))
-    op = _pool_tensor(pool, out, "out", _act(pool), (rows, hq, 128))
-    s = tab = kl = None
+    shape = (rows, hq, 128)
+    s = kl = tab = ks = kk = None
     if seqs is not None:
-        s = _i32(seqs)
-        if len(s) != n:
+        s, count, ks = _ints(seqs)
+        if count != n:
             raise ValueError("seqs and the query lengths differ in length")
     if kv_lens is not None:
-        kl = _i32(kv_lens)
-        if len(kl) != n:
+        kl, count, kk = _ints(kv_lens)
+        if count != n:
             raise ValueError("kv_lens and the query lengths differ in length")
     if block_tables is not None:
-        tab = _pool_tensor(pool, block_tables, "block_tables", torch.int32, (n, pool.max_blocks_per_seq))
-    args = [pool.handle, layer, n, s.ctypes.data if s is not None else None, tab,
-            kl.ctypes.data if kl is not None else None, m.ctypes.data]
-    if mask is not None:
-        args.append(_pool_tensor(pool, mask, "tree_mask", mask.dtype, (rows,)))
-    _check(fn(*args, hq, qp, op, scale, _pool_stream(pool, stream)), where)
+        tab = _pool_tensor(pool, block_tables, "block_tables", i32, (n, pool.max_blocks_per_seq))
+    return (n, s, tab, kl, m, hq, _pool_tensor(pool, q, "q", act, shape),
+            _pool_tensor(pool, out, "out", act, shape), rows, (keep, ks, kk))
 
 
 def pa_prefill_attention(pool: Pool, layer: int, q_lens, q, out, scale: float, seqs=None, kv_lens=None,
@@ -489,8 +519,10 @@ def pa_prefill_attention(pool: Pool, layer: int, q_lens, q, out, scale: float, s
     """Causal attention of the last q_lens[i] tokens of each sequence over its cached
     rows: q / out [sum(q_lens)][H_q][128].  The sequences are `seqs` of the pool, or
     `block_tables` (device int32 [n][max_blocks_per_seq]) with host `kv_lens` [n]."""
-    _attend(lib().pa_prefill_attention, "pa_prefill_attention", pool, layer, q_lens, None, q, out, scale, seqs,
-            kv_lens, block_tables, stream)
+    n, s, tab, kl, m, hq, qp, op, _, _keep = _attend_args(pool, q_lens, q, out, seqs, kv_lens, block_tables)
+    st = lib().pa_prefill_attention(pool.handle, layer, n, s, tab, kl, m, hq, qp, op, scale, _pool_stream(pool, stream))
+    if st != PA_OK:
+        _check(st, "pa_prefill_attention")
 
 
 def pa_tree_attention(pool: Pool, layer: int, tree_lens, tree_mask, q, out, scale: float, seqs=None,
@@ -499,11 +531,14 @@ def pa_tree_attention(pool: Pool, layer: int, tree_lens, tree_mask, q, out, scal
     tree: each attends the whole prefix and the drafts whose bits its word of
     `tree_mask` (int64 or uint64 device tensor [sum(tree_lens)]) sets.  Other
     arguments as pa_prefill_attention."""
-    import torch
-    if tree_mask.dtype not in (torch.int64, torch.uint64):
+    n, s, tab, kl, m, hq, qp, op, rows, _keep = _attend_args(pool, tree_lens, q, out, seqs, kv_lens, block_tables)
+    if tree_mask.element_size() != 8 or tree_mask.is_floating_point():
         raise ValueError("tree_mask must be an int64 or uint64 tensor")
-    _attend(lib().pa_tree_attention, "pa_tree_attention", pool, layer, tree_lens, tree_mask, q, out, scale, seqs,
-            kv_lens, block_tables, stream)
+    mp = _pool_tensor(pool, tree_mask, "tree_mask", tree_mask.dtype, (rows,))
+    st = lib().pa_tree_attention(pool.handle, layer, n, s, tab, kl, m, mp, hq, qp, op, scale,
+                                 _pool_stream(pool, stream))
+    if st != PA_OK:
+        _check(st, "pa_tree_attention")
 
 
 def pa_get_seq(pool: Pool, seq: int):

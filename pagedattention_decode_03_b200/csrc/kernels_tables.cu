@@ -117,13 +117,6 @@ __global__ void __launch_bounds__(kTablesThreads) build_tables_kernel(const __gr
     if (tt > prm.cap) bad |= kErrBadLen;
     fail_s = bad != 0;
     if (bad) atomicOr(prm.err, bad);
-    // every CTA has read the head before it counts itself in here, so the last
-    // one may replace it even where both pointers name the same word
-    __threadfence();
-    if (atomicAdd(prm.ticket, 1) == static_cast<int32_t>(gridDim.x) - 1) {
-      *prm.free_head_out = bad ? head : head + static_cast<int32_t>(tb);
-      *prm.ticket = 0;
-    }
   }
   int64_t et = bt + ct - st, eb = bb + cb - sb;
   for (int i = i0; i < i1; ++i) {
@@ -183,6 +176,17 @@ __global__ void __launch_bounds__(kTablesThreads) build_tables_kernel(const __gr
       const int32_t have = (old[i] + B - 1) >> prm.bshift;
       prm.tables[static_cast<int64_t>(i) * prm.mbps + have + (e - blk[i])] = prm.free_blocks[head + e];
     }
+  // Every CTA has read the head before it counts itself in here, so the last one
+  // may replace it even where both pointers name the same word.
+  if (tid == 0) {
+    bool last = gridDim.x == 1;
+    if (!last) {
+      __threadfence();
+      last = atomicAdd(prm.ticket, 1) == static_cast<int32_t>(gridDim.x) - 1;
+      if (last) *prm.ticket = 0;
+    }
+    if (last) *prm.free_head_out = failed ? head : head + blk[prm.n];
+  }
 }
 
 // ------------------------------------------------------------ append_slots
@@ -285,7 +289,7 @@ cudaError_t launch_build_tables(const PoolView& pool, int n, const int32_t* old_
     if (e != cudaSuccess) return e;
   }
   const int64_t per = kTablesThreads * kSlotsPerThread;
-  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(2 * num_sms, (cap + per - 1) / per)));
+  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4 * num_sms, (cap + per - 1) / per)));
   return launch_pdl(build_tables_kernel, dim3(grid), dim3(kTablesThreads), smem, stream, prm);
 }
 
