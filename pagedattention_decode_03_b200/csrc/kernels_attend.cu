@@ -23,7 +23,8 @@
 // Roles: warp 0 claims work and loads queries, warps 0 and 2 issue the KV tiles'
 // TMA copies, warp 1 issues the MMAs, warp 3 zeroes V rows past a length, warps 4-7 and 8-11 are the two
 // softmax streams (a thread owns a row: its running maximum and sum need no
-// exchange), warps 12-15 convert FP8 codes to the activation type.
+// exchange), warps 12-15 convert FP8 codes to fp16 (exact, one instruction a
+// pair; bf16 queries then become fp16 times a power of two a row).
 // Work units are claimed from a counter, longest first.  Where there are too
 // few units for the SMs the positions are split into chunks whose partial
 // results (O, maximum, sum) a second kernel joins.
@@ -48,14 +49,21 @@ constexpr int kOperand = 2 * kHalf;             // a 16-bit tile (32 KB)
 constexpr int kLoaders = 2;                     // warps that issue a tile's copies, 8 / kLoaders blocks each
 constexpr int kRaw = kTile * 128;               // an FP8 tile (16 KB)
 constexpr int kPartFloats = kHeadDim + 2;       // of one row: O, maximum, sum
-constexpr float kLazy = 8.f;                    // log2 units a row's maximum may pass its reference by
+// A row's weights are 2^(score - reference + kBias); its reference follows the
+// running maximum only when that passes it by kLazy (in log2 units).  bf16 has
+// fp32's range, so any lag will do; fp16 weights stay under 2^(kLazy + kBias) =
+// 2^15, and are normal numbers down to 2^-26 of the reference's.
+template <int MMA>
+constexpr float kLazy = MMA == kBF16 ? 8.f : 3.f;
+template <int MMA>
+constexpr float kBias = MMA == kBF16 ? 0.f : 12.f;
 
 // Ring depths: up to 224 KB of the SM's 227.
 template <bool PAIR, bool FP8>
 struct Ring {
   static constexpr int kQ = PAIR ? 2 : 1;
-  static constexpr int kStages = FP8 ? 3 : 5;
-  static constexpr int kRawStages = FP8 ? (PAIR ? 4 : 5) : 0;
+  static constexpr int kStages = FP8 ? 4 : 5;
+  static constexpr int kRawStages = FP8 ? (PAIR ? 2 : 3) : 0;
   static constexpr int kThreads = FP8 ? 512 : 384;
   // Registers a thread: at launch (65,536 over the threads), then by role.  The
   // softmax keeps a whole row of S; the shares add up to the launch's total.
@@ -85,10 +93,14 @@ struct Unit {
 struct Meta {
   uint64_t kv_full[6], kv_empty[6], raw_full[6], raw_empty[6];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], ml[2];
-  uint64_t sched_full[2], sched_empty[2], done, clean_go, clean_done;
+  uint64_t sched_full[2], sched_empty[2], done, clean_go, clean_done, q_ready[2];
   Unit unit[2];
   uint32_t tmem;
   int32_t abort;
+  // [unit % 4][stream][row]: queries are held as q 2^-exp (FP8 caches, bf16).  The
+  // queries of two units may be converted while a stream still works on the one
+  // before them (units of one or two tiles); a third waits for its epilogue.
+  int8_t q_exp[4][2][kTile];
   int32_t rows[kLoaders][8][8 / kLoaders];  // cache rows of the last 8 tiles' blocks
   float mlv[2][2][2][kTile];  // [unit parity][stream][max, sum][row] (dual)
 };
@@ -246,11 +258,12 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     attend_kernel(const __grid_constant__ Params prm, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq) {
   constexpr bool kFp8 = KV == kFP8;
+  constexpr int MMA = kFp8 ? kFP16 : ACT;        // type of the products' operands
+  constexpr bool kScaleQ = kFp8 && ACT == kBF16;
   using R = Ring<PAIR, kFp8>;
   constexpr int kLead = PAIR ? 1 : 2;           // K tiles copied ahead of the V tile of step i
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
+  uint8_t* sm = smem_raw + (-dev::smem_u32(smem_raw) & 1023u);
   Meta& mt = *reinterpret_cast<Meta*>(sm + R::kOffMeta);
   const uint32_t base = dev::smem_u32(sm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -279,6 +292,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
       dev::mbar_init(bar(mt.sched_empty[x]), kSchedConsumers);
     }
     dev::mbar_init(bar(mt.done), 1);
+    dev::mbar_init(bar(mt.q_ready[0]), 4);
+    dev::mbar_init(bar(mt.q_ready[1]), 4);
     dev::mbar_init(bar(mt.clean_go), 1);
     dev::mbar_init(bar(mt.clean_done), 1);
     mt.abort = 0;
@@ -495,7 +510,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     // One thread runs the whole role: what it does between two MMAs is time the
     // tensor core may stand still.
     if (dev::elect_one()) {
-      constexpr bool kBf = ACT == kBF16;
+      constexpr bool kBf = MMA == kBF16;
       constexpr uint32_t kIdS = instr_desc(kBf, false), kIdO = instr_desc(kBf, true);
       const uint64_t q_desc = smem_desc(base, 16, 1024), k_desc = smem_desc(base + R::kOffKv, 16, 1024),
                      v_desc = smem_desc(base + R::kOffKv, 2048, 1024);
@@ -569,7 +584,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
           const uint32_t k0 = take_k();
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (!ok || nx[x] == 0 || !wait1(mt.q_full[x], q_i[x] & 1)) continue;
+            if (!ok || nx[x] == 0 || !wait1(kScaleQ ? mt.q_ready[x] : mt.q_full[x], q_i[x] & 1)) continue;
             ++q_i[x];
             issue_s(x, k0);
             if (nx[x] == 1) commit(bar(mt.q_empty[x]));
@@ -595,7 +610,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
             }
           }
         } else {
-          if (!wait1(mt.q_full[0], q_i[0] & 1)) break;
+          if (!wait1(kScaleQ ? mt.q_ready[0] : mt.q_full[0], q_i[0] & 1)) break;
           ++q_i[0];
           for (int32_t i = 0; ok && i < min(2, n); ++i) {
             const uint32_t k = take_k();
@@ -656,7 +671,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t ts = tl + x * 128, to = tl + 256 + x * 128;
     const int32_t tq = kTile >> prm.gshift, G = 1 << prm.gshift;
-    uint32_t s_i = 0, o_i[2] = {0, 0}, ml_i = 0;
+    uint32_t s_i = 0, o_i[2] = {0, 0}, ml_i = 0, q_i = 0;
     Unit u;
     while (next_unit(u)) {
       const int32_t n = PAIR ? (x == 0 ? u.n0 : u.n1) : u.n0;   // this stream's last step + 1
@@ -681,15 +696,22 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         sl2 *= prm.k_scale[prm.layer * prm.H + u.h];
         vs = prm.v_scale[prm.layer * prm.H + u.h];
       }
-      if (sl2 == 0.f) sl2 = 1e-30f;                     // equal weights; a masked -inf x sl2 stays -inf
       const bool neg = sl2 < 0.f;
       const float none = neg ? INFINITY : -INFINITY;    // a masked score: -inf once scaled
+      if constexpr (!kScaleQ)
+        if (sl2 == 0.f) sl2 = 1e-30f;                   // equal weights; a masked -inf x sl2 stays -inf
       float mref = -INFINITY, l = 0.f;
       bool ok = true;
       for (int32_t i = PAIR ? 0 : x; i < n; i += PAIR ? 1 : 2) {
         if (!(ok = wait(mt.s_full[x], s_i & 1))) break;
         ++s_i;
         fence_after();
+        if constexpr (kScaleQ) {
+          if (i < (PAIR ? 1 : 2)) {                     // S is made from the converted queries
+            sl2 = ldexpf(sl2, mt.q_exp[q_i & 3][PAIR ? x : 0][r]);
+            if (sl2 == 0.f) sl2 = 1e-30f;
+          }
+        }
         if (warp_ok) {
           const int32_t p0 = (u.tile0 + i) * kTile;
           const bool masked = p0 + kTile > lim_min;
@@ -725,9 +747,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
             for (int k = 1; k < 8; ++k) mc[0] = fmaxf(mc[0], mc[k]);
           }
           const float mx = mc[0] * sl2;      // -inf where nothing is allowed
-          // the reference moves only when the maximum passes it by 2^8: O is
-          // then scaled, after the P V of the step before (complete: S came after it)
-          const bool move = mx > mref + kLazy || (mref == -INFINITY && mx > -INFINITY);
+          // where the reference moves, O is scaled to the new one, after the P V of the step before (complete: S came after it)
+          const bool move = mx > mref + kLazy<MMA> || (mref == -INFINITY && mx > -INFINITY);
           float corr = 1.f;
           if (move) {
             corr = mref == -INFINITY ? 0.f : dev::exp2_approx(mref - mx);
@@ -745,7 +766,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
               tmem_st16(to + c * 16, reinterpret_cast<const uint32_t(&)[16]>(o));
             }
           }
-          const float mr = mref == -INFINITY ? 0.f : -mref;
+          const float mr = mref == -INFINITY ? 0.f : kBias<MMA> - mref;
           const uint64_t sl2x2 = pack_f32x2(sl2, sl2), mrx2 = pack_f32x2(mr, mr);
           uint64_t ls[2] = {0, 0};
 #pragma unroll
@@ -758,7 +779,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
               e0 = dev::exp2_approx(e0);
               e1 = dev::exp2_approx(e1);
               ls[(k >> 1) & 1] = add_f32x2(ls[(k >> 1) & 1], pack_f32x2(e0, e1));
-              pk[k >> 1] = pack2<ACT>(e0, e1);
+              pk[k >> 1] = pack2<MMA>(e0, e1);
             }
             tmem_st16(ts + c * 16, pk);      // columns of S chunk c / 2, which is in registers
           }
@@ -772,6 +793,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         if (lane == 0) arrive(bar(mt.p_full[x]));
       }
       if (!ok) break;
+      ++q_i;
       // ---- epilogue
       uint16_t* out = reinterpret_cast<uint16_t*>(prm.out) +
                       ((static_cast<int64_t>(tok) * prm.H + u.h) * G + g) * kHeadDim;
@@ -852,8 +874,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     }
   } else if constexpr (kFp8) {
     regs_less<R::kRegsConvert>();
-    // ================================================ FP8 codes to 16-bit tiles
-    uint32_t raw_i = 0;
+    // ==================================================== FP8 codes to fp16 tiles
+    uint32_t raw_i = 0, q_i[2] = {0, 0};
     const int tid = threadIdx.x - 384;
     Unit u;
     bool ok = true;
@@ -864,28 +886,33 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         if (!wait(mt.raw_full[rs], (raw_i / (kFp8 ? R::kRawStages : 1)) & 1)) return false;
         if (!wait(mt.kv_empty[ks], ((raw_i / R::kStages) & 1) ^ 1)) return false;
         const int32_t valid = min(kTile, u.kv_len - (u.tile0 + i) * kTile);
-        const uint8_t* src = sm + R::kOffRaw + rs * kRaw;
-        uint8_t* dst = sm + R::kOffKv + ks * kOperand;
-#pragma unroll 2
+        // 16 codes, 16c .., of tokens t, t + 16, ...: every address is one of three
+        // bases plus a constant, and all loads are out before the first store.  All
+        // four warps share a tile: what counts is how soon one is ready.
+        const int t = tid >> 3, c = tid & 7, f = c >> 2;
+        const uint8_t* src = sm + R::kOffRaw + rs * kRaw + t * 128 + ((c ^ (t & 7)) << 4);
+        uint4 raw[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) raw[k] = *reinterpret_cast<const uint4*>(src + k * 2048);
+        if (is_v && valid < kTile) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k * 16 + t >= valid) raw[k] = make_uint4(0, 0, 0, 0);
+        }
+        uint8_t* row = sm + R::kOffKv + ks * kOperand + (is_v ? f * 2048 : f * kHalf) + t * 128;
+        const int step = is_v ? 4096 : 2048;
+        // the two d-halves write their chunks in opposite order: no bank is hit twice
+        uint8_t* d0 = row + (((2 * (c & 3) + f) ^ (t & 7)) << 4);
+        uint8_t* d1 = row + (((2 * (c & 3) + 1 - f) ^ (t & 7)) << 4);
+#pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int e = k * 128 + tid, tok = e >> 3, c = e & 7;      // 16 codes: 16c .. of token tok
-          uint4 raw = *reinterpret_cast<const uint4*>(src + tok * 128 + ((c ^ (tok & 7)) << 4));
-          if (is_v && tok >= valid) raw = make_uint4(0, 0, 0, 0);
-          const uint32_t wsrc[4] = {raw.x, raw.y, raw.z, raw.w};
+          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
           uint32_t o[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint32_t h2 = dev::e4m3x2_to_f16x2(static_cast<uint16_t>(wsrc[q >> 1] >> ((q & 1) * 16)));
-            o[q] = ACT == kBF16 ? dev::pack_bf16(dev::f16lo_to_f32(h2), dev::f16hi_to_f32(h2)) : h2;
-          }
-          uint8_t* row = is_v ? dst + (tok >> 4) * 4096 + (c >> 2) * 2048 + (tok & 15) * 128
-                              : dst + (c >> 2) * kHalf + tok * 128;
-          const int cc = 2 * (c & 3), sw = tok & 7;
-          // the two d-halves write their chunks in opposite order: no bank is hit twice
-          const int f = c >> 2;
+          for (int q = 0; q < 8; ++q) o[q] = dev::e4m3x2_to_f16x2(static_cast<uint16_t>(w[q >> 1] >> ((q & 1) * 16)));
           const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-          *reinterpret_cast<uint4*>(row + (((cc + f) ^ sw) << 4)) = f ? hi : lo;
-          *reinterpret_cast<uint4*>(row + (((cc + 1 - f) ^ sw) << 4)) = f ? lo : hi;
+          *reinterpret_cast<uint4*>(d0 + k * step) = f ? hi : lo;
+          *reinterpret_cast<uint4*>(d1 + k * step) = f ? lo : hi;
         }
         dev::fence_proxy_async_smem();
         __syncwarp();
@@ -896,6 +923,37 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         ++raw_i;
         return true;
       };
+      if constexpr (kScaleQ) {
+        // bf16 queries as fp16 times a power of two a row: the row's largest value
+        // goes to [2^14, 2^15), so all that is lost is under 2^-38 of it
+#pragma unroll
+        for (int x = 0; x < R::kQ; ++x) {
+          if (!ok || (x == 0 ? u.n0 : u.n1) == 0 || !(ok = wait(mt.q_full[x], q_i[x] & 1))) continue;
+          uint8_t* q = sm + x * kOperand + tid * 128;
+          uint32_t top = 0;                        // of |q|: bf16 magnitudes compare as integers
+#pragma unroll 4
+          for (int c = 0; c < 16; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(q + (c >> 3) * kHalf + (((c & 7) ^ (tid & 7)) << 4));
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                         __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+          }
+          top = max(top & 0xffffu, top >> 16) >> 7;                       // biased exponent
+          const int e = max(static_cast<int>(top) - 127 - 14, -126);
+          const float f = __int_as_float((127 - e) << 23);                // 2^-e
+          mt.q_exp[q_i[x] & 3][x][tid] = static_cast<int8_t>(e);
+#pragma unroll 4
+          for (int c = 0; c < 16; ++c) {
+            uint4* at = reinterpret_cast<uint4*>(q + (c >> 3) * kHalf + (((c & 7) ^ (tid & 7)) << 4));
+            const uint4 v = *at;
+            auto half2 = [&](uint32_t w) { return dev::pack_f16(dev::bf16lo_to_f32(w) * f, dev::bf16hi_to_f32(w) * f); };
+            *at = make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+          }
+          ++q_i[x];
+          dev::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive(bar(mt.q_ready[x]));
+        }
+      }
       for (int32_t i = 0; ok && i < min(kLead, n); ++i) ok = convert(i, false);
       for (int32_t i = 0; ok && i < n; ++i) {
         ok = convert(i, true);
@@ -1034,15 +1092,19 @@ cudaError_t launch_attend(const PoolView& pool, const CacheMaps& maps, const Att
   const int H = pool.num_kv_heads, G = a.num_q_heads / H;
   const int tq = kTile / G;
   const int n = items.n;
-  // units of one KV head, and the widest sequence, in each form
-  int64_t pair_units = 0;
+  // Pairs of query tiles read each KV tile once for 256 rows: taken where few
+  // of them stay half empty and their KV tiles still go round the SMs (below,
+  // one tile's two streams end sooner).
+  int64_t singles = 0, pairs = 0, pair_tiles = 0;
   int max_rows = 0;
   for (int i = 0; i < n; ++i) {
     const int m = items.q0[i + 1] - items.q0[i];
-    pair_units += ceil_div(m, 2 * tq);
+    singles += ceil_div(m, tq);
+    pairs += ceil_div(m, 2 * tq);
+    pair_tiles += static_cast<int64_t>(ceil_div(m, 2 * tq)) * ceil_div(items.kv_len[i], kTile);
     max_rows = std::max(max_rows, m * G);
   }
-  const bool pair = max_rows > kTile && pair_units * H >= num_sms;
+  const bool pair = 16 * pairs <= 9 * singles && (pairs * H >= num_sms || pair_tiles * H >= 16 * num_sms);
   const int kq = pair ? 2 : 1, ut = tq * kq;
 
   prm.out = static_cast<uint8_t*>(a.out);

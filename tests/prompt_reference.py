@@ -7,6 +7,10 @@ activation type and A = sum p |v| / sum p, the mean of |v| under the weights:
 * the weights enter the second product rounded to the activation type: u A
   (plus, for fp16, weights under 2^-14 of the row's reference are subnormal and
   carry an absolute error of 2^-25 each at most: 2^-25 x sum |v| / sum p);
+* an FP8 cache's products run on fp16 operands (codes are exact in fp16) with
+  weights up to 2^15, 2^12 at the row's reference or more: subnormal weights are
+  off by half of 2^-24 there, 2^-37 of the reference, which is not above the
+  row's maximum: 2^-37 x sum |v| / sum p with p relative to the maximum;
 * the exponential itself is held to a sixteenth of that: u A / 16;
 * scores are fp32 sums of 128 products; with the scale they are off by at most
   e = 130 x 2^-24 x scale x max sum |q_d k_d|, which moves every weight, and
@@ -129,6 +133,8 @@ class Setup:
                     bound = u * (1 + 1 / 16) * A + (2 * e[..., None] + 2 * (L + 8) * 2.0 ** -24) * A + u * ref.abs()
                     if self.act == "fp16":
                         bound = bound + 2.0 ** -25 * (seen.double() @ v[:, h].abs())[None] / one + 2.0 ** -25
+                    if self.kv == "fp8_e4m3":
+                        bound = bound + 2.0 ** -37 * (seen.double() @ v[:, h].abs())[None] / one
                     got = out[base + a:base + b, h * G:(h + 1) * G].double().permute(1, 0, 2)
                     assert torch.isfinite(got).all(), (what, i, a, h)
                     ratio = (got - ref).abs() / bound.clamp(min=1e-300)
