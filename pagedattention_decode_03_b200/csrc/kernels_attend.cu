@@ -34,6 +34,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "pa_internal.h"
@@ -62,15 +63,15 @@ constexpr float kBias = MMA == kBF16 ? 0.f : 12.f;
 template <bool PAIR, bool FP8>
 struct Ring {
   static constexpr int kQ = PAIR ? 2 : 1;
-  static constexpr int kStages = FP8 ? 4 : 5;
-  static constexpr int kRawStages = FP8 ? (PAIR ? 2 : 3) : 0;
+  static constexpr int kStages = FP8 ? (PAIR ? 3 : 4) : 5;
+  static constexpr int kRawStages = FP8 ? (PAIR ? 4 : 3) : 0;
   static constexpr int kThreads = FP8 ? 512 : 384;
   // Registers a thread: at launch (65,536 over the threads), then by role.  The
   // softmax keeps a whole row of S; the shares add up to the launch's total.
   static constexpr int kRegsLaunch = FP8 ? 128 : 168;
-  static constexpr int kRegsControl = FP8 ? 72 : 104;
-  static constexpr int kRegsSoftmax = FP8 ? 176 : 200;
-  static constexpr int kRegsConvert = FP8 ? 88 : 0;
+  static constexpr int kRegsControl = FP8 ? 64 : 104;
+  static constexpr int kRegsSoftmax = FP8 ? 184 : 200;
+  static constexpr int kRegsConvert = FP8 ? 80 : 0;
   static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsConvert <= kRegsLaunch * (kThreads / 128), "register shares");
   static constexpr int kOffKv = kQ * kOperand;
   static constexpr int kOffRaw = kOffKv + kStages * kOperand;
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
   constexpr bool kFp8 = KV == kFP8;
   constexpr int MMA = kFp8 ? kFP16 : ACT;        // type of the products' operands
   constexpr bool kScaleQ = kFp8 && ACT == kBF16;
+  constexpr bool kSpec = MMA == kBF16;
   using R = Ring<PAIR, kFp8>;
   constexpr int kLead = PAIR ? 1 : 2;           // K tiles copied ahead of the V tile of step i
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -732,60 +734,90 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
               for (int k = 0; k < 32; ++k) y[c][k] = a >> k & 1 ? y[c][k] : none;
             }
           }
-          float mc[8];
+          // Weights of the row against the reference, their sum, and (MAX) the row's
+          // maximum on the way: it runs beside the exponentials, which the
+          // special-function unit bounds.
+          const uint64_t sl2x2 = pack_f32x2(sl2, sl2);
+          float top;                             // of the scaled scores; -inf where nothing is allowed
+          auto weights = [&](auto with_max) {
+            constexpr bool MAX = decltype(with_max)::value;
+            const float mr = mref == -INFINITY ? 0.f : kBias<MMA> - mref;
+            const uint64_t mrx2 = pack_f32x2(mr, mr);
+            uint64_t ls[2] = {0, 0};
+            float mc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mc[k] = none;
-          if (neg) {
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int k = 0; k < 128; k += 2) mc[(k >> 1) & 7] = fminf(mc[(k >> 1) & 7], fminf(y[k >> 5][k & 31], y[k >> 5][(k & 31) + 1]));
-#pragma unroll
-            for (int k = 1; k < 8; ++k) mc[0] = fminf(mc[0], mc[k]);
+              for (int k = 0; k < 32; k += 2) {
+                float e0, e1;
+                unpack_f32x2(fma_f32x2(pack_f32x2(y[c][k], y[c][k + 1]), sl2x2, mrx2), e0, e1);
+                e0 = dev::exp2_approx(e0);
+                e1 = dev::exp2_approx(e1);
+                if (MAX) {
+                  float& m = mc[(k >> 1) & 3];
+                  m = fmaxf(m, fmaxf(y[c][k], y[c][k + 1]));
+                }
+                ls[(k >> 1) & 1] = add_f32x2(ls[(k >> 1) & 1], pack_f32x2(e0, e1));
+                pk[k >> 1] = pack2<MMA>(e0, e1);
+              }
+              tmem_st16(ts + c * 16, pk);        // over columns of S chunk c / 2, which is in registers
+            }
+            if (MAX) top = sl2 * fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+            float l0, l1;
+            unpack_f32x2(add_f32x2(ls[0], ls[1]), l0, l1);
+            return l0 + l1;
+          };
+          // A tile whose maximum does not pass the reference by kLazy, as nearly all
+          // after a row's first do, is done with the weights it was given at once.
+          const bool known = kSpec && !neg && __all_sync(0xffffffffu, !row_ok || mref > -INFINITY);
+          bool done = false;
+          if (known) {
+            if constexpr (kSpec) {
+              const float sum = weights(std::true_type{});
+              done = !__any_sync(0xffffffffu, row_ok && top > mref + kLazy<MMA>);
+              if (done) l += sum;
+            }
           } else {
+            float mc[8];
 #pragma unroll
-            for (int k = 0; k < 128; k += 2) mc[(k >> 1) & 7] = fmaxf(mc[(k >> 1) & 7], fmaxf(y[k >> 5][k & 31], y[k >> 5][(k & 31) + 1]));
+            for (int k = 0; k < 8; ++k) mc[k] = none;
+            if (neg) {
 #pragma unroll
-            for (int k = 1; k < 8; ++k) mc[0] = fmaxf(mc[0], mc[k]);
-          }
-          const float mx = mc[0] * sl2;      // -inf where nothing is allowed
-          // where the reference moves, O is scaled to the new one, after the P V of the step before (complete: S came after it)
-          const bool move = mx > mref + kLazy<MMA> || (mref == -INFINITY && mx > -INFINITY);
-          float corr = 1.f;
-          if (move) {
-            corr = mref == -INFINITY ? 0.f : dev::exp2_approx(mref - mx);
-            mref = mx;
-            l *= corr;
-          }
-          const bool first = i < (PAIR ? 1 : 2);
-          if (!first && __any_sync(0xffffffffu, move)) {
+              for (int k = 0; k < 128; k += 2) mc[(k >> 1) & 7] = fminf(mc[(k >> 1) & 7], fminf(y[k >> 5][k & 31], y[k >> 5][(k & 31) + 1]));
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              float o[16];
-              tmem_ld16(to + c * 16, o);
+              for (int k = 1; k < 8; ++k) mc[0] = fminf(mc[0], mc[k]);
+            } else {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= corr;
-              tmem_st16(to + c * 16, reinterpret_cast<const uint32_t(&)[16]>(o));
+              for (int k = 0; k < 128; k += 2) mc[(k >> 1) & 7] = fmaxf(mc[(k >> 1) & 7], fmaxf(y[k >> 5][k & 31], y[k >> 5][(k & 31) + 1]));
+#pragma unroll
+              for (int k = 1; k < 8; ++k) mc[0] = fmaxf(mc[0], mc[k]);
             }
+            top = sl2 * mc[0];
           }
-          const float mr = mref == -INFINITY ? 0.f : kBias<MMA> - mref;
-          const uint64_t sl2x2 = pack_f32x2(sl2, sl2), mrx2 = pack_f32x2(mr, mr);
-          uint64_t ls[2] = {0, 0};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float e0, e1;
-              unpack_f32x2(fma_f32x2(pack_f32x2(y[c][k], y[c][k + 1]), sl2x2, mrx2), e0, e1);
-              e0 = dev::exp2_approx(e0);
-              e1 = dev::exp2_approx(e1);
-              ls[(k >> 1) & 1] = add_f32x2(ls[(k >> 1) & 1], pack_f32x2(e0, e1));
-              pk[k >> 1] = pack2<MMA>(e0, e1);
+          if (!done) {
+            // the reference moves, and O is scaled to the new one, after the P V of the
+            // step before (complete: S came after it)
+            const bool move = top > mref + kLazy<MMA> || (mref == -INFINITY && top > -INFINITY);
+            float corr = 1.f;
+            if (move) {
+              corr = mref == -INFINITY ? 0.f : dev::exp2_approx(mref - top);
+              mref = top;
+              l *= corr;
             }
-            tmem_st16(ts + c * 16, pk);      // columns of S chunk c / 2, which is in registers
+            const bool first = i < (PAIR ? 1 : 2);
+            if (!first && __any_sync(0xffffffffu, move)) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                float o[16];
+                tmem_ld16(to + c * 16, o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] *= corr;
+                tmem_st16(to + c * 16, reinterpret_cast<const uint32_t(&)[16]>(o));
+              }
+            }
+            l += weights(std::false_type{});
           }
-          float l0, l1;
-          unpack_f32x2(add_f32x2(ls[0], ls[1]), l0, l1);
-          l += l0 + l1;
           tmem_wait_st();
         }
         fence_before();
@@ -1093,18 +1125,19 @@ cudaError_t launch_attend(const PoolView& pool, const CacheMaps& maps, const Att
   const int tq = kTile / G;
   const int n = items.n;
   // Pairs of query tiles read each KV tile once for 256 rows: taken where few
-  // of them stay half empty and their KV tiles still go round the SMs (below,
-  // one tile's two streams end sooner).
-  int64_t singles = 0, pairs = 0, pair_tiles = 0;
+  // of them stay half empty and there is one for each SM (else one tile's two
+  // streams, with the positions split, keep more SMs busy: trees of 20 to 33
+  // drafts over 32K FP8 tokens, 80 pairs, 665 us as pairs and 482 us as single
+  // tiles; ragged prompts, 8B class, 882 us as pairs and 1064 us as single tiles).
+  int64_t singles = 0, pairs = 0;
   int max_rows = 0;
   for (int i = 0; i < n; ++i) {
     const int m = items.q0[i + 1] - items.q0[i];
     singles += ceil_div(m, tq);
     pairs += ceil_div(m, 2 * tq);
-    pair_tiles += static_cast<int64_t>(ceil_div(m, 2 * tq)) * ceil_div(items.kv_len[i], kTile);
     max_rows = std::max(max_rows, m * G);
   }
-  const bool pair = 16 * pairs <= 9 * singles && (pairs * H >= num_sms || pair_tiles * H >= 16 * num_sms);
+  const bool pair = 16 * pairs <= 9 * singles && pairs * H >= num_sms;
   const int kq = pair ? 2 : 1, ut = tq * kq;
 
   prm.out = static_cast<uint8_t*>(a.out);
