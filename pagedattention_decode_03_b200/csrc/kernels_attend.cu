@@ -919,9 +919,10 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         if (!wait(mt.kv_empty[ks], ((raw_i / R::kStages) & 1) ^ 1)) return false;
         const int32_t valid = min(kTile, u.kv_len - (u.tile0 + i) * kTile);
         // 16 codes, 16c .., of tokens t, t + 16, ...: every address is one of three
-        // bases plus a constant, and all loads are out before the first store.  All
-        // four warps share a tile: what counts is how soon one is ready.
-        const int t = tid >> 3, c = tid & 7, f = c >> 2;
+        // bases plus a constant, and all loads are out before the first store.  Eight
+        // lanes hold eight tokens, which the swizzle spreads over the banks.  All four
+        // warps share a tile: what counts is how soon one is ready.
+        const int t = (tid & 7) + (tid >> 6) * 8, c = (tid >> 3) & 7, f = c >> 2;
         const uint8_t* src = sm + R::kOffRaw + rs * kRaw + t * 128 + ((c ^ (t & 7)) << 4);
         uint4 raw[8];
 #pragma unroll
@@ -932,20 +933,23 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
             if (k * 16 + t >= valid) raw[k] = make_uint4(0, 0, 0, 0);
         }
         uint8_t* row = sm + R::kOffKv + ks * kOperand + (is_v ? f * 2048 : f * kHalf) + t * 128;
-        const int step = is_v ? 4096 : 2048;
-        // the two d-halves write their chunks in opposite order: no bank is hit twice
-        uint8_t* d0 = row + (((2 * (c & 3) + f) ^ (t & 7)) << 4);
-        uint8_t* d1 = row + (((2 * (c & 3) + 1 - f) ^ (t & 7)) << 4);
+        uint8_t* d0 = row + (((2 * (c & 3)) ^ (t & 7)) << 4);
+        uint8_t* d1 = row + (((2 * (c & 3) + 1) ^ (t & 7)) << 4);
+        auto store = [&](auto step) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-          uint32_t o[8];
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+            uint32_t o[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) o[q] = dev::e4m3x2_to_f16x2(static_cast<uint16_t>(w[q >> 1] >> ((q & 1) * 16)));
-          const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-          *reinterpret_cast<uint4*>(d0 + k * step) = f ? hi : lo;
-          *reinterpret_cast<uint4*>(d1 + k * step) = f ? lo : hi;
-        }
+            for (int q = 0; q < 8; ++q) o[q] = dev::e4m3x2_to_f16x2(static_cast<uint16_t>(w[q >> 1] >> ((q & 1) * 16)));
+            *reinterpret_cast<uint4*>(d0 + k * decltype(step)::value) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(d1 + k * decltype(step)::value) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        };
+        if (is_v)
+          store(std::integral_constant<int, 4096>{});
+        else
+          store(std::integral_constant<int, 2048>{});
         dev::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
