@@ -102,6 +102,7 @@ struct pa_pool {
   bool dev_ready = false;
   int num_sms = 0;
   pa::CacheMaps maps{};
+  pa::AttendMaps attend_maps{};
   uint64_t launches = 0;
   // scratch reused across calls
   std::vector<pa::CowPair> cows;
@@ -141,6 +142,9 @@ pa_status ensure_device(pa_pool* p, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p->d.num_layers) * p->d.num_blocks * p->d.num_kv_heads *
                        p->d.block_size;
   if (const char* why = pa::encode_cache_maps(p->d.k_cache, p->d.v_cache, p->d.kv_dtype, rows, &p->maps))
+    return fail(PA_ERR_CUDA, why);
+  if (const char* why = pa::encode_attend_maps(p->d.k_cache, p->d.v_cache, p->d.kv_dtype, p->d.block_size, rows,
+                                               &p->attend_maps))
     return fail(PA_ERR_CUDA, why);
   p->dev_ready = true;
   return PA_OK;
@@ -1050,7 +1054,7 @@ pa_status attend_call(pa_pool* p, const char* what, bool tree, int32_t layer, in
     if (items.n == 0) break;
     row += items.q0[items.n];
     int launches = 0;
-    const cudaError_t e = pa::launch_attend(p->view, p->maps, args, items, p->num_sms, s, &launches);
+    const cudaError_t e = pa::launch_attend(p->view, p->attend_maps, args, items, p->num_sms, s, &launches);
     p->launches += launches;
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   }

@@ -46,6 +46,7 @@ constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 128;                      // rows of a query tile, positions of a KV tile
 constexpr int kHalf = kTile * 128;              // one 64-element d-half of a 16-bit tile (16 KB)
+constexpr int kGroup = 8 * 128;                 // 8 tokens of one d-half in a KV tile (1 KB)
 constexpr int kOperand = 2 * kHalf;             // a 16-bit tile (32 KB)
 constexpr int kLoaders = 2;                     // warps that issue a tile's copies, 8 / kLoaders blocks each
 constexpr int kRaw = kTile * 128;               // an FP8 tile (16 KB)
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&mt.tmem);
-  dev::grid_dep_wait();
+  // (each role that touches global memory waits for the kernel before this one
+  // first; the schedule's first unit comes from the parameters alone)
 
   // A warp's bounded wait, one outcome for all lanes; false ends the role.
   auto wait = [&](uint64_t& b, uint32_t parity) {
@@ -354,52 +356,48 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
   // ------------------------------------------------------------------ loaders
   // KV tiles in ring order: K(0 .. kLead-1), then V(i), K(i + kLead), ...  One
   // warp gets a copy out every ~60 ns (a lane at a time), so kLoaders warps share
-  // each tile's blocks.  16-bit tiles: K as two boxes a block, [2 d-halves][128]
-  // [128 B] (the rows of a d-half must be evenly spaced for the MMA); V, whose
-  // MMA takes one 16-token block a step, as one box of both d-halves a block.
+  // each tile's blocks and a block comes as one box.  A 16-bit box lies as
+  // [8-token groups][2 d-halves][8 tokens][128 B]: the groups of a d-half are then
+  // evenly spaced over the whole tile, as the MMA wants its rows.
   constexpr uint32_t kDepth = kFp8 ? R::kRawStages : R::kStages;
-  constexpr int kShare = 8 / kLoaders;
   uint32_t ring_i = 0;
   auto load_unit = [&](const Unit& u) {
     const int part = warp >> 1;                                      // warps 0, 2
     const int32_t n = max(u.n0, u.n1);
     const int32_t* table = prm.tables + static_cast<int64_t>(u.seq_row) * prm.mbps;
-    const int32_t blocks = (u.kv_len + 15) >> 4;                     // of 16 tokens
-    int32_t id = 0, id_base = -64;
+    const int32_t blocks = (u.kv_len + (16 << prm.bshift) - 1) >> (4 + prm.bshift);
+    const int32_t per_log = 3 - prm.bshift, share = (1 << per_log) / kLoaders;   // blocks a tile, and of this warp
+    const int32_t bytes = (kFp8 ? 2048 : 4096) << prm.bshift;                    // of a block
+    int32_t id = 0, id_base = -64;                                   // cache rows of blocks id_base + lane
     auto copy = [&](int32_t i, bool is_v) {
-      const int32_t b0 = (u.tile0 + i) * 8, nb = max(0, min(kShare, blocks - b0 - part * kShare));
+      const int32_t b0 = (u.tile0 + i) << per_log, nb = max(0, min(share, blocks - b0 - part * share));
       if (!is_v) {  // the tile's cache rows, kept for its V copy
         if (b0 >= id_base + 32 || id_base < 0) {
           id_base = b0;
-          const int32_t b = b0 + lane, e = b >> prm.bshift;
-          int32_t v = b < blocks && e < prm.mbps ? table[e] : 0;
+          const int32_t b = b0 + lane;
+          int32_t v = b < blocks && b < prm.mbps ? table[b] : 0;
           if (static_cast<uint32_t>(v) >= static_cast<uint32_t>(prm.num_blocks)) {
             atomicOr(prm.err, kErrBadBlock);
             v = 0;
           }
-          id = (((prm.layer * prm.num_blocks + v) * prm.H + u.h) << (4 + prm.bshift)) +
-               (b & ((1 << prm.bshift) - 1)) * 16;
+          id = ((prm.layer * prm.num_blocks + v) * prm.H + u.h) << (4 + prm.bshift);
         }
-        const int32_t row = __shfl_sync(0xffffffffu, id, (b0 - id_base + part * kShare + lane) & 31);
-        if (lane < kShare) mt.rows[part][i & 7][lane] = row;
+        const int32_t row = __shfl_sync(0xffffffffu, id, (b0 - id_base + part * share + lane) & 31);
+        if (lane < share) mt.rows[part][i & 7][lane] = row;
         __syncwarp();
       }
       const uint32_t st = ring_i % kDepth, par = ((ring_i / kDepth) & 1) ^ 1;
       if (!wait(kFp8 ? mt.raw_empty[st] : mt.kv_empty[st], par)) return false;
       const uint32_t full = bar(kFp8 ? mt.raw_full[st] : mt.kv_full[st]);
-      if (lane == 0) dev::mbar_arrive_expect_tx(full, nb * (kFp8 ? 2048 : 4096));
+      if (lane == 0) dev::mbar_arrive_expect_tx(full, nb * bytes);
       __syncwarp();  // the bytes are expected before any copy is issued
-      const int j = lane % kShare, half = lane / kShare;
-      const uint32_t dst = base + (kFp8 ? R::kOffRaw + st * kRaw : R::kOffKv + st * kOperand);
-      if (j < nb) {
-        const int32_t row = mt.rows[part][i & 7][j], jb = part * kShare + j;
-        if (kFp8) {
-          if (half == 0) dev::tma_load_2d(dst + jb * 2048, is_v ? &tmv : &tmk, 0, row, full);
-        } else if (is_v) {
-          if (half == 0) dev::tma_load_3d(dst + jb * 4096, &tmv, 0, row, 0, full);
-        } else if (half < 2) {
-          dev::tma_load_2d(dst + half * kHalf + jb * 2048, &tmk, half * 64, row, full);
-        }
+      if (lane < nb) {
+        const int32_t row = mt.rows[part][i & 7][lane];
+        const uint32_t dst = base + (kFp8 ? R::kOffRaw + st * kRaw : R::kOffKv + st * kOperand) + (part * share + lane) * bytes;
+        if (kFp8)
+          dev::tma_load_2d(dst, is_v ? &tmv : &tmk, 0, row, full);
+        else
+          dev::tma_load_4d(dst, is_v ? &tmv : &tmk, 0, 0, 0, row >> 3, full);
       }
       ++ring_i;
       return true;
@@ -421,6 +419,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
   if (warp < 4) {
   regs_less<R::kRegsControl>();
   if (warp == 2) {
+    dev::grid_dep_wait();
     Unit u;
     while (next_unit(u) && load_unit(u)) {
     }
@@ -432,13 +431,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     bool ok = true;
     const int32_t total = prm.units;
     const int32_t tq = kTile >> prm.gshift;       // tokens of a query tile
-    for (;;) {
-      // the claim after this one is on its way while this unit is copied
-      if (lane == 0 && w < total) {
-        const int32_t v = atomicAdd(prm.counter, 1);
-        if (v == total - 1) *prm.counter = 0;     // the last claim of all: `units` claims in total
-        w_next = static_cast<int32_t>(gridDim.x) + v;
-      }
+    for (bool begun = false;; begun = true) {
       Unit u;
       u.seq_row = -1;
       if (w < total) {
@@ -473,6 +466,13 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         }
         u.n0 = nx[0];
         u.n1 = nx[1];
+      }
+      if (!begun) dev::grid_dep_wait();
+      // the next claim is on its way while this unit is copied
+      if (lane == 0 && w < total) {
+        const int32_t v = atomicAdd(prm.counter, 1);
+        if (v == total - 1) *prm.counter = 0;     // the last claim of all: `units` claims in total
+        w_next = static_cast<int32_t>(gridDim.x) + v;
       }
       const int32_t n = u.seq_row < 0 ? 0 : max(u.n0, u.n1);
       if (u.seq_row < 0 || n > 0) {                                  // an empty chunk is skipped
@@ -514,8 +514,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     if (dev::elect_one()) {
       constexpr bool kBf = MMA == kBF16;
       constexpr uint32_t kIdS = instr_desc(kBf, false), kIdO = instr_desc(kBf, true);
-      const uint64_t q_desc = smem_desc(base, 16, 1024), k_desc = smem_desc(base + R::kOffKv, 16, 1024),
-                     v_desc = smem_desc(base + R::kOffKv, 2048, 1024);
+      const uint64_t q_desc = smem_desc(base, 16, 1024), k_desc = smem_desc(base + R::kOffKv, 16, 2 * kGroup),
+                     v_desc = smem_desc(base + R::kOffKv, kGroup, 2 * kGroup);
       uint32_t st = 0, ph = 0;                          // ring stage of the next tile, and its phase
       uint32_t q_i[2] = {0, 0}, p_i[2] = {0, 0}, o_i[2] = {0, 0}, clean_i = 0;
       bool ok = true;
@@ -544,8 +544,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         const uint64_t qd = q_desc + (PAIR ? x : 0) * (kOperand >> 4), kd = k_desc + s * (kOperand >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + x * 128, qd + o, kd + o, kIdS, kk > 0);
+          mma_ss(tmem + x * 128, qd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
+                 kd + (((kk >> 2) * kGroup + (kk & 3) * 32) >> 4), kIdS, kk > 0);
         }
         commit(bar(mt.s_full[x]));
       };
@@ -657,9 +657,12 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
       if (!wait(mt.clean_go, clean_i & 1)) break;
       ++clean_i;
       const int32_t valid = u.kv_len - (u.tile0 + n - 1) * kTile;
-      uint8_t* v = sm + R::kOffKv + ((kv_i - 1) % R::kStages) * kOperand + (valid >> 4) * 4096 + (valid & 15) * 128;
-      for (int c = lane; c < (16 - (valid & 15)) * 16; c += 32)
-        *reinterpret_cast<uint4*>(v + (c & 1) * 2048 + (c >> 4) * 128 + ((c >> 1) & 7) * 16) = make_uint4(0, 0, 0, 0);
+      uint8_t* v = sm + R::kOffKv + ((kv_i - 1) % R::kStages) * kOperand;
+      for (int c = lane; c < (16 - (valid & 15)) * 16; c += 32) {
+        const int t = valid + (c >> 4);
+        *reinterpret_cast<uint4*>(v + (t >> 3) * 2 * kGroup + (c & 1) * kGroup + (t & 7) * 128 + ((c >> 1) & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
       dev::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive(bar(mt.clean_done));
@@ -674,6 +677,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     const uint32_t ts = tl + x * 128, to = tl + 256 + x * 128;
     const int32_t tq = kTile >> prm.gshift, G = 1 << prm.gshift;
     uint32_t s_i = 0, o_i[2] = {0, 0}, ml_i = 0, q_i = 0;
+    dev::grid_dep_wait();
     Unit u;
     while (next_unit(u)) {
       const int32_t n = PAIR ? (x == 0 ? u.n0 : u.n1) : u.n0;   // this stream's last step + 1
@@ -932,24 +936,18 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
           for (int k = 0; k < 8; ++k)
             if (k * 16 + t >= valid) raw[k] = make_uint4(0, 0, 0, 0);
         }
-        uint8_t* row = sm + R::kOffKv + ks * kOperand + (is_v ? f * 2048 : f * kHalf) + t * 128;
+        uint8_t* row = sm + R::kOffKv + ks * kOperand + (t >> 3) * 2 * kGroup + f * kGroup + (t & 7) * 128;
         uint8_t* d0 = row + (((2 * (c & 3)) ^ (t & 7)) << 4);
         uint8_t* d1 = row + (((2 * (c & 3) + 1) ^ (t & 7)) << 4);
-        auto store = [&](auto step) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-            uint32_t o[8];
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+          uint32_t o[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) o[q] = dev::e4m3x2_to_f16x2(static_cast<uint16_t>(w[q >> 1] >> ((q & 1) * 16)));
-            *reinterpret_cast<uint4*>(d0 + k * decltype(step)::value) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(d1 + k * decltype(step)::value) = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-        };
-        if (is_v)
-          store(std::integral_constant<int, 4096>{});
-        else
-          store(std::integral_constant<int, 2048>{});
+          for (int q = 0; q < 8; ++q) o[q] = dev::e4m3x2_to_f16x2(static_cast<uint16_t>(w[q >> 1] >> ((q & 1) * 16)));
+          *reinterpret_cast<uint4*>(d0 + k * 4 * kGroup) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(d1 + k * 4 * kGroup) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
         dev::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -1038,25 +1036,33 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant
   auto at = [&](int c) {
     return prm.partials + (((w0 + static_cast<int64_t>(c) * prm.H) * kq + x) * prm.part_rows + r) * kPartFloats;
   };
+  // lane c holds chunk c's weight; the rows then come without waiting for one another
   float mx = -INFINITY;
   for (int c = lane; c < chunks; c += 32) mx = fmaxf(mx, __ldcg(at(c) + kHeadDim));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-  for (int c = 0; c < chunks; ++c) {
-    const float* p = at(c);
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + kHeadDim));
-    if (ml.y > 0.f) {
-      const float w = dev::exp2_approx(ml.x - mx);
-      const float2 a = __ldcg(reinterpret_cast<const float2*>(p) + lane * 2);
-      const float2 b = __ldcg(reinterpret_cast<const float2*>(p) + lane * 2 + 1);
+  for (int c0 = 0; c0 < chunks; c0 += 32) {
+    float w = 0.f;
+    if (c0 + lane < chunks) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(at(c0 + lane) + kHeadDim));
+      w = ml.y > 0.f ? dev::exp2_approx(ml.x - mx) : 0.f;
       l += w * ml.y;
-      o[0] += w * a.x;
-      o[1] += w * a.y;
-      o[2] += w * b.x;
-      o[3] += w * b.y;
+    }
+    const int m = min(32, chunks - c0);
+#pragma unroll 8
+    for (int c = 0; c < m; ++c) {
+      const float2* p = reinterpret_cast<const float2*>(at(c0 + c)) + lane * 2;
+      const float2 a = __ldcg(p), b = __ldcg(p + 1);
+      const float wc = __shfl_sync(0xffffffffu, w, c);
+      o[0] += wc * a.x;
+      o[1] += wc * a.y;
+      o[2] += wc * b.x;
+      o[3] += wc * b.y;
     }
   }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
   const float inv = l > 0.f ? 1.f / l : 0.f;
   uint16_t* out = reinterpret_cast<uint16_t*>(prm.out) + ((static_cast<int64_t>(prm.row0) + k) * hq + qh) * kHeadDim;
   *reinterpret_cast<uint2*>(out + lane * 4) =
@@ -1081,7 +1087,7 @@ EncodeTiledFn encoder() {
 }
 
 template <int KV, int ACT, bool PAIR>
-cudaError_t run(const Params& prm, const CacheMaps& maps, const CUtensorMap& tmq, int num_sms, cudaStream_t stream) {
+cudaError_t run(const Params& prm, const AttendMaps& maps, const CUtensorMap& tmq, int num_sms, cudaStream_t stream) {
   using R = Ring<PAIR, KV == kFP8>;
   constexpr size_t smem = smem_bytes<PAIR, KV == kFP8>();
   static_assert(smem <= 227 * 1024, "attention exceeds the shared memory of an SM");
@@ -1101,11 +1107,11 @@ cudaError_t run(const Params& prm, const CacheMaps& maps, const CUtensorMap& tmq
     if (dev < 64) configured |= uint64_t{1} << dev;
   }
   return launch_pdl(attend_kernel<KV, ACT, PAIR>, dim3(std::min(num_sms, prm.units)), dim3(R::kThreads), smem, stream,
-                    prm, maps.k, maps.v3, tmq);
+                    prm, maps.k, maps.v, tmq);
 }
 
 template <bool PAIR>
-cudaError_t dispatch(const PoolView& pool, const Params& prm, const CacheMaps& maps, const CUtensorMap& tmq,
+cudaError_t dispatch(const PoolView& pool, const Params& prm, const AttendMaps& maps, const CUtensorMap& tmq,
                      int num_sms, cudaStream_t stream) {
   const bool bf = pool.act_dtype == kBF16;
   if (pool.kv_dtype == kFP8)
@@ -1119,7 +1125,7 @@ int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 }  // namespace
 
-cudaError_t launch_attend(const PoolView& pool, const CacheMaps& maps, const AttendArgs& a, const AttendItems& items,
+cudaError_t launch_attend(const PoolView& pool, const AttendMaps& maps, const AttendArgs& a, const AttendItems& items,
                           int num_sms, cudaStream_t stream, int* launches) {
   EncodeTiledFn encode = encoder();
   if (!encode) return cudaErrorNotSupported;
@@ -1164,7 +1170,8 @@ cudaError_t launch_attend(const PoolView& pool, const CacheMaps& maps, const Att
   prm.part_rows = pair ? kTile : std::min(kTile, (max_rows + 7) / 8 * 8);
 
   // KV tiles of a chunk: all of a sequence's, unless the units are too few for
-  // the SMs; then the smallest chunk that gives each SM one
+  // the SMs; then the smallest chunk that gives each SM one, if that saves more
+  // tiles (~1 us each) than joining the chunks costs (a second kernel, ~4 us).
   auto count = [&](int chunk) {
     int64_t u = 0;
     for (int i = 0; i < n; ++i)
@@ -1175,16 +1182,16 @@ cudaError_t launch_attend(const PoolView& pool, const CacheMaps& maps, const Att
   int most = 1;
   for (int i = 0; i < n; ++i) most = std::max(most, ceil_div(items.kv_len[i], kTile));
   int chunk = most;
-  constexpr int kMinChunk = 4;
+  constexpr int kMinChunk = 4, kJoin = 5;
   const int64_t room = pool.partial_slots * kPartialSlotFloats / (static_cast<int64_t>(prm.part_rows) * kPartFloats * kq);
   const int64_t want = std::min<int64_t>(num_sms, room);
-  if (count(most) < want && most > kMinChunk) {
+  if (count(most) < want && most >= kMinChunk + kJoin) {
     int lo = kMinChunk, hi = most;                // the smallest chunk with count <= want
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
       if (count(mid) <= want) hi = mid; else lo = mid + 1;
     }
-    chunk = lo;
+    if (lo + kJoin <= most) chunk = lo;
   }
   prm.chunk = chunk;
   const int64_t units = count(chunk);

@@ -201,7 +201,17 @@ struct AttendArgs {
   float scale;
 };
 
-cudaError_t launch_attend(const PoolView& pool, const CacheMaps& maps, const AttendArgs& args,
+// Its tensor maps of the cache (tensor_maps.cpp): one box is one block of one KV
+// head.  16-bit: the 4-D view [8-row groups][2 d-halves][8 rows][64], box {64, 8,
+// 2, block_size / 8}; FP8: the 2-D view [rows][128], box {128, block_size}.
+struct AttendMaps {
+  CUtensorMap k, v;
+};
+// Returns null on success, else what failed.
+const char* encode_attend_maps(void* k_cache, void* v_cache, int kv_dtype, int block_size, int64_t rows,
+                               AttendMaps* maps);
+
+cudaError_t launch_attend(const PoolView& pool, const AttendMaps& maps, const AttendArgs& args,
                           const AttendItems& items, int num_sms, cudaStream_t stream, int* launches);
 
 // Thread-local text returned by pa_last_error() (defined in api.cpp).

@@ -72,4 +72,29 @@ const char* encode_cache_maps(void* k_cache, void* v_cache, int kv_dtype, int64_
   return nullptr;
 }
 
+const char* encode_attend_maps(void* k_cache, void* v_cache, int kv_dtype, int block_size, int64_t rows,
+                               AttendMaps* m) {
+  EncodeTiledFn encode = encoder();
+  if (!encode) return "cuTensorMapEncodeTiled not available from the driver";
+  const bool fp8 = kv_dtype == kFP8;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  // FP8: rows of 128 bytes
+  const cuuint64_t dims2[2] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides2[1] = {static_cast<cuuint64_t>(kHeadDim)};
+  const cuuint32_t box2[2] = {128u, static_cast<cuuint32_t>(block_size)};
+  // 16-bit: d of a half, row of a group, half, group of 8 rows
+  const cuuint64_t dims4[4] = {64, 8, 2, static_cast<cuuint64_t>(rows / 8)};
+  const cuuint64_t strides4[3] = {256, 128, 2048};
+  const cuuint32_t box4[4] = {64u, 8u, 2u, static_cast<cuuint32_t>(block_size / 8)};
+  void* base[2] = {k_cache, v_cache};
+  CUtensorMap* map[2] = {&m->k, &m->v};
+  for (int i = 0; i < 2; ++i)
+    if (encode(map[i], fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, fp8 ? 2 : 4, base[i],
+               fp8 ? dims2 : dims4, fp8 ? strides2 : strides4, fp8 ? box2 : box4, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return "cuTensorMapEncodeTiled (block view) failed";
+  return nullptr;
+}
+
 }  // namespace pa
