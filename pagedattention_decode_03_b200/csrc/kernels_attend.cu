@@ -50,7 +50,7 @@ constexpr int kGroup = 8 * 128;                 // 8 tokens of one d-half in a K
 constexpr int kOperand = 2 * kHalf;             // a 16-bit tile (32 KB)
 constexpr int kLoaders = 2;                     // warps that issue a tile's copies, 8 / kLoaders blocks each
 constexpr int kRaw = kTile * 128;               // an FP8 tile (16 KB)
-constexpr int kPartFloats = kHeadDim + 2;       // of one row: O, maximum, sum
+constexpr int kPartFloats = kHeadDim + 2;       // of one row: O, maximum, sum, each a line of rows
 // A row's weights are 2^(score - reference + kBias); its reference follows the
 // running maximum only when that passes it by kLazy (in log2 units).  bf16 has
 // fp32's range, so any lag will do; fp16 weights stay under 2^(kLazy + kBias) =
@@ -833,7 +833,9 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
       // ---- epilogue
       uint16_t* out = reinterpret_cast<uint16_t*>(prm.out) +
                       ((static_cast<int64_t>(tok) * prm.H + u.h) * G + g) * kHeadDim;
-      float* part = prm.partials + (static_cast<int64_t>(u.part + (PAIR ? x : 0)) * prm.part_rows + r) * kPartFloats;
+      // partial: [130][part_rows], so that a warp's rows lie side by side
+      const int64_t pr = prm.part_rows;
+      float* part = prm.partials + static_cast<int64_t>(u.part + (PAIR ? x : 0)) * pr * kPartFloats + r;
       const bool direct = u.direct >> (PAIR ? x : 0) & 1;
       auto put = [&](int c, const float (&o)[32]) {  // columns 32c.. of this row
         if (!row_ok) return;
@@ -845,7 +847,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
                            pack2<ACT>(o[k + 6], o[k + 7]));
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) *reinterpret_cast<float2*>(part + c * 32 + k) = make_float2(o[k], o[k + 1]);
+          for (int k = 0; k < 32; ++k) part[(c * 32 + k) * pr] = o[k];
         }
       };
       if constexpr (PAIR) {
@@ -865,7 +867,10 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         fence_before();
         __syncwarp();
         if (lane == 0) arrive(bar(mt.o_free[x]));
-        if (!direct && row_ok) *reinterpret_cast<float2*>(part + kHeadDim) = make_float2(mref, l);
+        if (!direct && row_ok) {
+          part[kHeadDim * pr] = mref;
+          part[(kHeadDim + 1) * pr] = l;
+        }
       } else {
         // join the two streams; stream x writes d-half x
         bool all = true;
@@ -905,7 +910,10 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         fence_before();
         __syncwarp();
         if (lane == 0) arrive(bar(mt.o_free[0]));
-        if (!direct && row_ok && x == 0) *reinterpret_cast<float2*>(part + kHeadDim) = make_float2(mm, lsum);
+        if (!direct && row_ok && x == 0) {
+          part[kHeadDim * pr] = mm;
+          part[(kHeadDim + 1) * pr] = lsum;
+        }
       }
     }
   } else if constexpr (kFp8) {
@@ -1003,70 +1011,76 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
 }
 
 // ------------------------------------------------------------- joining chunks
-// One warp per (token, query head) of a sequence that was split: the chunks'
-// O are weighted by 2^(their maximum - the row's) and divided by the sum.
-template <int ACT>
-__global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant__ Params prm, int tokens, int kq) {
+// A thread takes one row and D d of one query tile, a warp 32 rows side by side,
+// and the loads of several chunks are under way together: they are all this kernel
+// waits for.  The chunks' O are weighted by 2^(their maximum - the row's) and
+// divided by the sum.  Tiles that had one chunk are done already.
+template <int ACT, int D>
+__global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant__ Params prm, int kq) {
+  constexpr int kCtas = 64 / D, kBatch = 32 / D;  // CTAs of a query tile; chunks whose loads are under way together
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = 1 << prm.gshift;
+  const int32_t b = blockIdx.x, dq = b % kCtas, x = (b / kCtas) % kq, v = b / kCtas / kq;
+  const int32_t h = v % prm.H, tq = kTile >> prm.gshift, ut = tq * kq;
+  int32_t tile = v / prm.H, it = 0, qt = 0;       // the tile's sequence, and its place there (few sequences are split)
+  for (; it < prm.n; ++it) {
+    qt = (prm.m[it] + ut - 1) / ut;
+    if (tile < qt) break;
+    tile -= qt;
+  }
+  if (it == prm.n) return;
+  const int32_t m = prm.m[it], past = prm.kv_len[it] - m, t0 = tile * ut + x * tq;
+  if (t0 >= m) return;
+  const int32_t last = prm.mask ? prm.kv_len[it] - 1 : past + min(t0 + tq, m) - 1;
+  const int32_t nt = last / kTile + 1;
+  if (nt <= prm.chunk) return;
+  const int32_t chunks = (nt + prm.chunk - 1) / prm.chunk, ch = (prm.pre[it + 1] - prm.pre[it]) / qt;
+  const int64_t w = static_cast<int64_t>(prm.pre[it] + (qt - 1 - tile) * ch) * prm.H + h;
+  const int32_t r = (warp & 3) * 32 + lane, t = t0 + (r >> prm.gshift);
   dev::grid_dep_wait();
   dev::grid_dep_launch();
-  const int lane = threadIdx.x & 31, G = 1 << prm.gshift, hq = prm.H << prm.gshift;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(tokens) * hq) return;
-  const int32_t k = static_cast<int32_t>(row / hq), qh = static_cast<int32_t>(row % hq);
-  const int32_t h = qh >> prm.gshift, g = qh & (G - 1);
-  // items lie in the order of their work, not of their tokens: find the one that holds token k
-  int it = -1;
-  for (int i0 = 0; i0 < prm.n && it < 0; i0 += 32) {
-    const int i = i0 + lane;
-    const unsigned hit = __ballot_sync(0xffffffffu, i < prm.n && prm.q0[min(i, prm.n - 1)] <= k &&
-                                                        k < prm.q0[min(i, prm.n - 1)] + prm.m[min(i, prm.n - 1)]);
-    if (hit) it = i0 + __ffs(hit) - 1;
-  }
-  if (it < 0) return;
-  const int32_t tq = kTile >> prm.gshift, ut = tq * kq;
-  const int32_t t = k - prm.q0[it], m = prm.m[it], past = prm.kv_len[it] - m;
-  const int32_t tile = t / ut, x = (t - tile * ut) / tq;
-  const int32_t last = prm.mask ? prm.kv_len[it] - 1 : past + min(tile * ut + (x + 1) * tq, m) - 1;
-  const int32_t nt = last / kTile + 1;
-  if (nt <= prm.chunk) return;                    // written by its only chunk
-  const int32_t chunks = (nt + prm.chunk - 1) / prm.chunk;
-  const int32_t qt = (m + ut - 1) / ut, ch = (prm.pre[it + 1] - prm.pre[it]) / qt;
-  const int64_t w0 = (static_cast<int64_t>(prm.pre[it]) + (qt - 1 - tile) * ch) * prm.H + h;
-  const int32_t r = (t - tile * ut - x * tq) * G + g;
-  auto at = [&](int c) {
-    return prm.partials + (((w0 + static_cast<int64_t>(c) * prm.H) * kq + x) * prm.part_rows + r) * kPartFloats;
-  };
-  // lane c holds chunk c's weight; the rows then come without waiting for one another
-  float mx = -INFINITY;
-  for (int c = lane; c < chunks; c += 32) mx = fmaxf(mx, __ldcg(at(c) + kHeadDim));
+  if (t >= m) return;
+  const int64_t pr = prm.part_rows, step = static_cast<int64_t>(prm.H) * kq * pr * kPartFloats;   // to the next chunk
+  const float* part = prm.partials + (w * kq + x) * pr * kPartFloats + r;
+  const int d0 = dq * 2 * D + (warp >> 2) * D;
+  float mx = -INFINITY, o[D], l = 0.f;            // the sum so far, against the running maximum
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-  for (int c0 = 0; c0 < chunks; c0 += 32) {
-    float w = 0.f;
-    if (c0 + lane < chunks) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(at(c0 + lane) + kHeadDim));
-      w = ml.y > 0.f ? dev::exp2_approx(ml.x - mx) : 0.f;
-      l += w * ml.y;
+  for (int k = 0; k < D; ++k) o[k] = 0.f;
+  for (int c0 = 0; c0 < chunks; c0 += kBatch) {
+    float mc[kBatch], lc[kBatch], vc[kBatch][D];
+#pragma unroll
+    for (int c = 0; c < kBatch; ++c) {
+      const bool in = c0 + c < chunks;
+      const float* p = part + (c0 + c) * step;
+      mc[c] = in ? __ldcg(p + kHeadDim * pr) : -INFINITY;
+      lc[c] = in ? __ldcg(p + (kHeadDim + 1) * pr) : 0.f;
+#pragma unroll
+      for (int k = 0; k < D; ++k) vc[c][k] = in ? __ldcg(p + (d0 + k) * pr) : 0.f;
     }
-    const int m = min(32, chunks - c0);
-#pragma unroll 8
-    for (int c = 0; c < m; ++c) {
-      const float2* p = reinterpret_cast<const float2*>(at(c0 + c)) + lane * 2;
-      const float2 a = __ldcg(p), b = __ldcg(p + 1);
-      const float wc = __shfl_sync(0xffffffffu, w, c);
-      o[0] += wc * a.x;
-      o[1] += wc * a.y;
-      o[2] += wc * b.x;
-      o[3] += wc * b.y;
+    float top = mx;
+#pragma unroll
+    for (int c = 0; c < kBatch; ++c) top = fmaxf(top, mc[c]);
+    const float corr = mx == -INFINITY ? 0.f : dev::exp2_approx(mx - top);
+    mx = top;
+    l *= corr;
+#pragma unroll
+    for (int k = 0; k < D; ++k) o[k] *= corr;
+#pragma unroll
+    for (int c = 0; c < kBatch; ++c) {
+      const float wc = lc[c] > 0.f ? dev::exp2_approx(mc[c] - mx) : 0.f;
+      l += wc * lc[c];
+#pragma unroll
+      for (int k = 0; k < D; ++k) o[k] += wc * vc[c][k];
     }
   }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint16_t* out = reinterpret_cast<uint16_t*>(prm.out) + ((static_cast<int64_t>(prm.row0) + k) * hq + qh) * kHeadDim;
-  *reinterpret_cast<uint2*>(out + lane * 4) =
-      make_uint2(pack2<ACT>(o[0] * inv, o[1] * inv), pack2<ACT>(o[2] * inv, o[3] * inv));
+  uint32_t* out = reinterpret_cast<uint32_t*>(
+      prm.out + 2 * (((static_cast<int64_t>(prm.row0 + prm.q0[it] + t) * prm.H + h) * G + (r & (G - 1))) * kHeadDim + d0));
+  uint32_t res[D / 2];
+#pragma unroll
+  for (int k = 0; k < D / 2; ++k) res[k] = pack2<ACT>(o[2 * k] * inv, o[2 * k + 1] * inv);
+#pragma unroll
+  for (int k = 0; k < D / 2; k += 4)
+    *reinterpret_cast<uint4*>(out + k) = make_uint4(res[k], res[k + 1], res[k + 2], res[k + 3]);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1182,7 +1196,7 @@ cudaError_t launch_attend(const PoolView& pool, const AttendMaps& maps, const At
   int most = 1;
   for (int i = 0; i < n; ++i) most = std::max(most, ceil_div(items.kv_len[i], kTile));
   int chunk = most;
-  constexpr int kMinChunk = 4, kJoin = 5;
+  constexpr int kMinChunk = 2, kJoin = 5;
   const int64_t room = pool.partial_slots * kPartialSlotFloats / (static_cast<int64_t>(prm.part_rows) * kPartFloats * kq);
   const int64_t want = std::min<int64_t>(num_sms, room);
   if (count(most) < want && most >= kMinChunk + kJoin) {
@@ -1227,10 +1241,22 @@ cudaError_t launch_attend(const PoolView& pool, const AttendMaps& maps, const At
   if (e != cudaSuccess) return e;
   ++*launches;
   if (chunk < most) {
-    const int tokens = items.q0[n];
-    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(tokens) * a.num_q_heads + 7) / 8));
-    e = pool.act_dtype == kBF16 ? launch_pdl(attend_merge_kernel<kBF16>, grid, dim3(256), 0, stream, prm, tokens, kq)
-                                : launch_pdl(attend_merge_kernel<kFP16>, grid, dim3(256), 0, stream, prm, tokens, kq);
+    // Few tiles: more CTAs a tile (one of 32K tokens, 8 heads: 34 us in all with 8 d
+    // a thread, 37 with 16; 32 to 64 tiles of 4K to 8K: 23 and 69 us with 8, 22 and
+    // 66 with 16).
+    int64_t tiles = 0;
+    for (int i = 0; i < n; ++i) tiles += ceil_div(items.q0[i + 1] - items.q0[i], ut);
+    tiles *= H * kq;
+    const bool bf = pool.act_dtype == kBF16;
+    if (tiles < 32) {
+      const dim3 grid(static_cast<unsigned>(tiles * 8));
+      e = bf ? launch_pdl(attend_merge_kernel<kBF16, 8>, grid, dim3(256), 0, stream, prm, kq)
+             : launch_pdl(attend_merge_kernel<kFP16, 8>, grid, dim3(256), 0, stream, prm, kq);
+    } else {
+      const dim3 grid(static_cast<unsigned>(tiles * 4));
+      e = bf ? launch_pdl(attend_merge_kernel<kBF16, 16>, grid, dim3(256), 0, stream, prm, kq)
+             : launch_pdl(attend_merge_kernel<kFP16, 16>, grid, dim3(256), 0, stream, prm, kq);
+    }
     if (e != cudaSuccess) return e;
     ++*launches;
   }
