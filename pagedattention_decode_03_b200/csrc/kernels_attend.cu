@@ -112,6 +112,9 @@ constexpr size_t smem_bytes() {
   return 1024 + Ring<PAIR, FP8>::kOffMeta + sizeof(Meta) - (PAIR ? sizeof(Meta::mlv) : 0);
 }
 
+// Launch parameters, with room for CAP sequences: a call of few does not carry
+// the tables of many (10 KB: 1 to 2 us a launch on the host).
+template <int CAP>
 struct Params {
   uint8_t* out;
   const int32_t* tables;
@@ -127,11 +130,11 @@ struct Params {
   int32_t chunk;            // KV tiles of a chunk
   int32_t part_rows;        // rows of a partial
   int32_t n, row0;
-  int32_t row[kAttendItemsCap];
-  int32_t kv_len[kAttendItemsCap];
-  int32_t q0[kAttendItemsCap];       // first query token, and
-  int32_t m[kAttendItemsCap];        // how many
-  int32_t pre[kAttendItemsCap + 1];  // prefix of (query tiles x chunks), per KV head
+  int32_t row[CAP];
+  int32_t kv_len[CAP];
+  int32_t q0[CAP];         // first query token, and
+  int32_t m[CAP];          // how many
+  int32_t pre[CAP + 1];    // prefix of (query tiles x chunks), per KV head
 };
 
 // ------------------------------------------------------------------- tcgen05
@@ -255,9 +258,11 @@ __device__ __forceinline__ uint32_t low_bits(int32_t n) {
 }
 
 // ------------------------------------------------------------------- kernel
-template <int KV, int ACT, bool PAIR>
+constexpr int kSmallCap = 48;
+
+template <int KV, int ACT, bool PAIR, int CAP>
 __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
-    attend_kernel(const __grid_constant__ Params prm, const __grid_constant__ CUtensorMap tmk,
+    attend_kernel(const __grid_constant__ Params<CAP> prm, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq) {
   constexpr bool kFp8 = KV == kFP8;
   constexpr int MMA = kFp8 ? kFP16 : ACT;        // type of the products' operands
@@ -1015,8 +1020,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
 // and the loads of several chunks are under way together: they are all this kernel
 // waits for.  The chunks' O are weighted by 2^(their maximum - the row's) and
 // divided by the sum.  Tiles that had one chunk are done already.
-template <int ACT, int D>
-__global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant__ Params prm, int kq) {
+template <int ACT, int D, int CAP>
+__global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant__ Params<CAP> prm, int kq) {
   constexpr int kCtas = 64 / D, kBatch = 32 / D;  // CTAs of a query tile; chunks whose loads are under way together
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = 1 << prm.gshift;
   const int32_t b = blockIdx.x, dq = b % kCtas, x = (b / kCtas) % kq, v = b / kCtas / kq;
@@ -1100,8 +1105,8 @@ EncodeTiledFn encoder() {
   return fn;
 }
 
-template <int KV, int ACT, bool PAIR>
-cudaError_t run(const Params& prm, const AttendMaps& maps, const CUtensorMap& tmq, int num_sms, cudaStream_t stream) {
+template <int KV, int ACT, bool PAIR, int CAP>
+cudaError_t run(const Params<CAP>& prm, const AttendMaps& maps, const CUtensorMap& tmq, int num_sms, cudaStream_t stream) {
   using R = Ring<PAIR, KV == kFP8>;
   constexpr size_t smem = smem_bytes<PAIR, KV == kFP8>();
   static_assert(smem <= 227 * 1024, "attention exceeds the shared memory of an SM");
@@ -1110,41 +1115,40 @@ cudaError_t run(const Params& prm, const AttendMaps& maps, const CUtensorMap& tm
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(configured >> dev & 1u)) {
-    e = cudaFuncSetAttribute(attend_kernel<KV, ACT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attend_kernel<KV, ACT, PAIR, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     // the warpgroups' register shares come out of what the launch holds
     cudaFuncAttributes attr;
-    e = cudaFuncGetAttributes(&attr, attend_kernel<KV, ACT, PAIR>);
+    e = cudaFuncGetAttributes(&attr, attend_kernel<KV, ACT, PAIR, CAP>);
     if (e != cudaSuccess) return e;
     if (attr.numRegs < R::kRegsLaunch) return cudaErrorInvalidConfiguration;
     if (dev < 64) configured |= uint64_t{1} << dev;
   }
-  return launch_pdl(attend_kernel<KV, ACT, PAIR>, dim3(std::min(num_sms, prm.units)), dim3(R::kThreads), smem, stream,
+  return launch_pdl(attend_kernel<KV, ACT, PAIR, CAP>, dim3(std::min(num_sms, prm.units)), dim3(R::kThreads), smem, stream,
                     prm, maps.k, maps.v, tmq);
 }
 
-template <bool PAIR>
-cudaError_t dispatch(const PoolView& pool, const Params& prm, const AttendMaps& maps, const CUtensorMap& tmq,
+template <bool PAIR, int CAP>
+cudaError_t dispatch(const PoolView& pool, const Params<CAP>& prm, const AttendMaps& maps, const CUtensorMap& tmq,
                      int num_sms, cudaStream_t stream) {
   const bool bf = pool.act_dtype == kBF16;
   if (pool.kv_dtype == kFP8)
-    return bf ? run<kFP8, kBF16, PAIR>(prm, maps, tmq, num_sms, stream)
-              : run<kFP8, kFP16, PAIR>(prm, maps, tmq, num_sms, stream);
-  return bf ? run<kBF16, kBF16, PAIR>(prm, maps, tmq, num_sms, stream)
-            : run<kFP16, kFP16, PAIR>(prm, maps, tmq, num_sms, stream);
+    return bf ? run<kFP8, kBF16, PAIR, CAP>(prm, maps, tmq, num_sms, stream)
+              : run<kFP8, kFP16, PAIR, CAP>(prm, maps, tmq, num_sms, stream);
+  return bf ? run<kBF16, kBF16, PAIR, CAP>(prm, maps, tmq, num_sms, stream)
+            : run<kFP16, kFP16, PAIR, CAP>(prm, maps, tmq, num_sms, stream);
 }
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-}  // namespace
-
-cudaError_t launch_attend(const PoolView& pool, const AttendMaps& maps, const AttendArgs& a, const AttendItems& items,
-                          int num_sms, cudaStream_t stream, int* launches) {
+template <int CAP>
+cudaError_t launch(const PoolView& pool, const AttendMaps& maps, const AttendArgs& a, const AttendItems& items,
+                   int num_sms, cudaStream_t stream, int* launches) {
   EncodeTiledFn encode = encoder();
   if (!encode) return cudaErrorNotSupported;
-  static thread_local Params prm;
-  static thread_local int order[kAttendItemsCap];
+  static thread_local Params<CAP> prm;
+  static thread_local int order[CAP];
   const int H = pool.num_kv_heads, G = a.num_q_heads / H;
   const int tq = kTile / G;
   const int n = items.n;
@@ -1236,8 +1240,8 @@ cudaError_t launch_attend(const PoolView& pool, const AttendMaps& maps, const At
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  cudaError_t e = pair ? dispatch<true>(pool, prm, maps, tmq, num_sms, stream)
-                       : dispatch<false>(pool, prm, maps, tmq, num_sms, stream);
+  cudaError_t e = pair ? dispatch<true, CAP>(pool, prm, maps, tmq, num_sms, stream)
+                       : dispatch<false, CAP>(pool, prm, maps, tmq, num_sms, stream);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (chunk < most) {
@@ -1250,17 +1254,25 @@ cudaError_t launch_attend(const PoolView& pool, const AttendMaps& maps, const At
     const bool bf = pool.act_dtype == kBF16;
     if (tiles < 32) {
       const dim3 grid(static_cast<unsigned>(tiles * 8));
-      e = bf ? launch_pdl(attend_merge_kernel<kBF16, 8>, grid, dim3(256), 0, stream, prm, kq)
-             : launch_pdl(attend_merge_kernel<kFP16, 8>, grid, dim3(256), 0, stream, prm, kq);
+      e = bf ? launch_pdl(attend_merge_kernel<kBF16, 8, CAP>, grid, dim3(256), 0, stream, prm, kq)
+             : launch_pdl(attend_merge_kernel<kFP16, 8, CAP>, grid, dim3(256), 0, stream, prm, kq);
     } else {
       const dim3 grid(static_cast<unsigned>(tiles * 4));
-      e = bf ? launch_pdl(attend_merge_kernel<kBF16, 16>, grid, dim3(256), 0, stream, prm, kq)
-             : launch_pdl(attend_merge_kernel<kFP16, 16>, grid, dim3(256), 0, stream, prm, kq);
+      e = bf ? launch_pdl(attend_merge_kernel<kBF16, 16, CAP>, grid, dim3(256), 0, stream, prm, kq)
+             : launch_pdl(attend_merge_kernel<kFP16, 16, CAP>, grid, dim3(256), 0, stream, prm, kq);
     }
     if (e != cudaSuccess) return e;
     ++*launches;
   }
   return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_attend(const PoolView& pool, const AttendMaps& maps, const AttendArgs& args,
+                          const AttendItems& items, int num_sms, cudaStream_t stream, int* launches) {
+  return items.n <= kSmallCap ? launch<kSmallCap>(pool, maps, args, items, num_sms, stream, launches)
+                              : launch<kAttendItemsCap>(pool, maps, args, items, num_sms, stream, launches);
 }
 
 }  // namespace pa
