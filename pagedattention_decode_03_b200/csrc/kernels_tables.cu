@@ -28,7 +28,6 @@ namespace {
 // for the table entries another one writes.
 constexpr int kTablesThreads = 512;
 constexpr int kTablesWarps = kTablesThreads / 32;
-constexpr int kSlotsPerThread = 4;
 
 struct TablesParams {
   const int32_t* old_lens;
@@ -54,6 +53,8 @@ __device__ __forceinline__ int last_at_or_below(const int32_t* pre, int n, int32
   return lo;
 }
 
+// SPT: consecutive slots of a thread, which share a search and mostly a block.
+template <int SPT>
 __global__ void __launch_bounds__(kTablesThreads) build_tables_kernel(const __grid_constant__ TablesParams prm) {
   extern __shared__ int32_t sm[];
   int32_t* tok = sm;                  // [n + 1] tokens before request i
@@ -139,35 +140,39 @@ __global__ void __launch_bounds__(kTablesThreads) build_tables_kernel(const __gr
   const int64_t gid = static_cast<int64_t>(blockIdx.x) * kTablesThreads + tid;
   const int64_t gsize = static_cast<int64_t>(gridDim.x) * kTablesThreads;
   const int32_t total = failed ? 0 : tok[prm.n];
-  for (int64_t t0 = gid * kSlotsPerThread; t0 < prm.cap; t0 += gsize * kSlotsPerThread) {
-    int32_t v[kSlotsPerThread];
+  const bool aligned = (reinterpret_cast<uintptr_t>(prm.slots) & 15) == 0;
+  for (int64_t t0 = gid * SPT; t0 < prm.cap; t0 += gsize * SPT) {
     int i = t0 < total ? last_at_or_below(tok, prm.n, static_cast<int32_t>(t0)) : 0;
     int32_t lb0 = -1, i_of = -1, phys = 0;
 #pragma unroll
-    for (int k = 0; k < kSlotsPerThread; ++k) {
-      const int64_t t = t0 + k;
-      v[k] = -1;
-      if (t >= total) continue;
-      while (tok[i + 1] <= t) ++i;
-      const int32_t pos = old[i] + static_cast<int32_t>(t) - tok[i];
-      const int32_t lb = pos >> prm.bshift;
-      if (lb != lb0 || i != i_of) {
-        const int32_t have = (old[i] + B - 1) >> prm.bshift;
-        phys = lb < have ? prm.tables[static_cast<int64_t>(i) * prm.mbps + lb]
-                         : prm.free_blocks[head + blk[i] + lb - have];
-        lb0 = lb;
-        i_of = i;
-        if (static_cast<uint32_t>(phys) >= static_cast<uint32_t>(prm.num_blocks)) atomicOr(prm.err, kErrBadBlock);
-      }
-      if (static_cast<uint32_t>(phys) < static_cast<uint32_t>(prm.num_blocks))
-        v[k] = (phys << prm.bshift) + (pos & (B - 1));
-    }
-    if (t0 + kSlotsPerThread <= prm.cap && (reinterpret_cast<uintptr_t>(prm.slots) & 15) == 0) {
-      *reinterpret_cast<int4*>(prm.slots + t0) = make_int4(v[0], v[1], v[2], v[3]);
-    } else {
+    for (int q = 0; q < SPT; q += 4) {
+      int32_t v[4];
 #pragma unroll
-      for (int k = 0; k < kSlotsPerThread; ++k)
-        if (t0 + k < prm.cap) prm.slots[t0 + k] = v[k];
+      for (int k = 0; k < 4; ++k) {
+        const int64_t t = t0 + q + k;
+        v[k] = -1;
+        if (t >= total) continue;
+        while (tok[i + 1] <= t) ++i;
+        const int32_t pos = old[i] + static_cast<int32_t>(t) - tok[i];
+        const int32_t lb = pos >> prm.bshift;
+        if (lb != lb0 || i != i_of) {
+          const int32_t have = (old[i] + B - 1) >> prm.bshift;
+          phys = lb < have ? prm.tables[static_cast<int64_t>(i) * prm.mbps + lb]
+                           : prm.free_blocks[head + blk[i] + lb - have];
+          lb0 = lb;
+          i_of = i;
+          if (static_cast<uint32_t>(phys) >= static_cast<uint32_t>(prm.num_blocks)) atomicOr(prm.err, kErrBadBlock);
+        }
+        if (static_cast<uint32_t>(phys) < static_cast<uint32_t>(prm.num_blocks))
+          v[k] = (phys << prm.bshift) + (pos & (B - 1));
+      }
+      if (aligned && t0 + q + 4 <= prm.cap) {
+        *reinterpret_cast<int4*>(prm.slots + t0 + q) = make_int4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (t0 + q + k < prm.cap) prm.slots[t0 + q + k] = v[k];
+      }
     }
   }
   if (!failed)
@@ -283,14 +288,19 @@ cudaError_t launch_build_tables(const PoolView& pool, int n, const int32_t* old_
   prm.num_blocks = pool.num_blocks;
   prm.cap = cap;
   const size_t smem = (static_cast<size_t>(n) * 3 + 2) * sizeof(int32_t);
+  // Few slots: 4 a thread, for the shortest way through one CTA's.  Many: 16, one
+  // block's worth, so that a search and a block id serve them all: 509 prompts with
+  // 1 M slots 7.9 us; 4 a thread on two or four CTAs an SM took 8.4 and 10.9 us.
+  const bool many = cap > num_sms * kTablesThreads * 4;
+  auto* kernel = many ? build_tables_kernel<16> : build_tables_kernel<4>;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>((kTablesMaxSeqs * 3 + 2) * sizeof(int32_t)));
     if (e != cudaSuccess) return e;
   }
-  const int64_t per = kTablesThreads * kSlotsPerThread;
-  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4 * num_sms, (cap + per - 1) / per)));
-  return launch_pdl(build_tables_kernel, dim3(grid), dim3(kTablesThreads), smem, stream, prm);
+  const int64_t per = kTablesThreads * (many ? 16 : 4);
+  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms, (cap + per - 1) / per)));
+  return launch_pdl(kernel, dim3(grid), dim3(kTablesThreads), smem, stream, prm);
 }
 
 cudaError_t launch_append_slots(const PoolView& pool, int layer, int T, const int32_t* slots, const void* k_new,
