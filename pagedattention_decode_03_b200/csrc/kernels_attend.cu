@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
   // evenly spaced over the whole tile, as the MMA wants its rows.
   constexpr uint32_t kDepth = kFp8 ? R::kRawStages : R::kStages;
   uint32_t ring_i = 0;
-  auto load_unit = [&](const Unit& u) {
+  auto load_unit = [&](const Unit& u, auto between) {
     const int part = warp >> 1;                                      // warps 0, 2
     const int32_t n = max(u.n0, u.n1);
     const int32_t* table = prm.tables + static_cast<int64_t>(u.seq_row) * prm.mbps;
@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     };
     for (int32_t i = 0; i < min(kLead, n); ++i)
       if (!copy(i, false)) return false;
+    if (!between()) return false;
     for (int32_t i = 0; i < n; ++i) {
       if (!copy(i, true)) return false;
       if (i + kLead < n && !copy(i + kLead, false)) return false;
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
   if (warp == 2) {
     dev::grid_dep_wait();
     Unit u;
-    while (next_unit(u) && load_unit(u)) {
+    while (next_unit(u) && load_unit(u, [] { return true; })) {
     }
     load_drain();
   } else if (warp == 0) {
@@ -490,21 +491,24 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
       }
       if (u.seq_row < 0) break;
       if (n > 0) {
-        // query tiles: [2 d-halves][128 rows][128 B], row = token * G + head
+        // query tiles, [2 d-halves][128 rows][128 B], row = token * G + head: after the
+        // first K tiles, which need not wait for the tiles of the unit before
+        auto load_q = [&]() {
 #pragma unroll
-        for (int x = 0; x < R::kQ; ++x) {
-          if ((x == 0 ? u.n0 : u.n1) == 0) continue;
-          if (!(ok = wait(mt.q_empty[x], (q_i[x] & 1) ^ 1))) break;
-          if (lane == 0) {
-            const uint32_t dst = base + x * kOperand, b = bar(mt.q_full[x]);
-            dev::mbar_arrive_expect_tx(b, kOperand);
-            dev::tma_load_3d(dst, &tmq, 0, u.h << prm.gshift, u.tok0 + x * tq, b);
-            dev::tma_load_3d(dst + kHalf, &tmq, 64, u.h << prm.gshift, u.tok0 + x * tq, b);
+          for (int x = 0; x < R::kQ; ++x) {
+            if ((x == 0 ? u.n0 : u.n1) == 0) continue;
+            if (!wait(mt.q_empty[x], (q_i[x] & 1) ^ 1)) return false;
+            if (lane == 0) {
+              const uint32_t dst = base + x * kOperand, b = bar(mt.q_full[x]);
+              dev::mbar_arrive_expect_tx(b, kOperand);
+              dev::tma_load_3d(dst, &tmq, 0, u.h << prm.gshift, u.tok0 + x * tq, b);
+              dev::tma_load_3d(dst + kHalf, &tmq, 64, u.h << prm.gshift, u.tok0 + x * tq, b);
+            }
+            ++q_i[x];
           }
-          ++q_i[x];
-        }
-        if (!ok) break;
-        if (!(ok = load_unit(u))) break;
+          return true;
+        };
+        if (!(ok = load_unit(u, load_q))) break;
       }
       w = __shfl_sync(0xffffffffu, w_next, 0);
     }
@@ -842,14 +846,22 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
       const int64_t pr = prm.part_rows;
       float* part = prm.partials + static_cast<int64_t>(u.part + (PAIR ? x : 0)) * pr * kPartFloats + r;
       const bool direct = u.direct >> (PAIR ? x : 0) & 1;
+      const bool wide = (reinterpret_cast<uintptr_t>(prm.out) & 31) == 0;  // `out` itself may be 16-byte aligned
       auto put = [&](int c, const float (&o)[32]) {  // columns 32c.. of this row
         if (!row_ok) return;
         if (direct) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            *reinterpret_cast<uint4*>(out + c * 32 + k) =
-                make_uint4(pack2<ACT>(o[k], o[k + 1]), pack2<ACT>(o[k + 2], o[k + 3]), pack2<ACT>(o[k + 4], o[k + 5]),
-                           pack2<ACT>(o[k + 6], o[k + 7]));
+          for (int k = 0; k < 32; k += 16) {        // whole 32-byte sectors: a row is a line of its own
+            uint32_t v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = pack2<ACT>(o[k + 2 * e], o[k + 2 * e + 1]);
+            if (wide) {
+              dev::st_global_v8(out + c * 32 + k, v);
+            } else {
+              *reinterpret_cast<uint4*>(out + c * 32 + k) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(out + c * 32 + k + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+            }
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) part[(c * 32 + k) * pr] = o[k];

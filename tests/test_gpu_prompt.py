@@ -216,6 +216,21 @@ def test_rows_around_the_call_stay():
     assert (out[:20] == 7).all() and (out[155:] == 7).all()
 
 
+@pytest.mark.parametrize("lens,new", [([130, 5], [130, 5]), ([9000], [20]), ([2000] * 10, [600] * 10)])
+def test_queries_and_output_at_sixteen_byte_addresses(lens, new):
+    """q and out need 16-byte alignment, not more (whole, split and paired tiles)."""
+    s = Setup(lens, H=4, seed=1)
+    rows = sum(new)
+    q = torch.empty(rows * 16 * 128 + 8, dtype=DT["bf16"], device="cuda")[8:].view(rows, 16, 128)
+    whole = torch.full((rows * 16 * 128 + 16,), 7.0, dtype=DT["bf16"], device="cuda")
+    out = whole[8:-8].view(rows, 16, 128)
+    assert q.data_ptr() % 32 == 16 and out.data_ptr() % 32 == 16
+    q.copy_(s.rand(rows, 16, 2.0))
+    pa.pa_prefill_attention(s.pool, 0, new, q, out, SCALE, kv_lens=lens, block_tables=s.tables)
+    s.check(new, q, out, SCALE)
+    assert (whole[:8] == 7).all() and (whole[-8:] == 7).all()
+
+
 def test_other_stream_and_graph_replay():
     lens, new = [600, 9000, 64], [600, 16, 64]
     s = Setup(lens, H=2, seed=5)
