@@ -252,6 +252,13 @@ __device__ __forceinline__ void regs_less() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Weight of a part of a row with maximum m and sum l, against the maximum of all
+// parts: 0 for a part that attended nothing, NaN for one with a NaN in it (whose
+// maximum may be -inf).
+__device__ __forceinline__ float stream_weight(float m, float l, float all) {
+  return l == 0.f ? 0.f : (l == l ? dev::exp2_approx(m - all) : l);
+}
+
 // Columns of a 32-column chunk whose first n are allowed.
 __device__ __forceinline__ uint32_t low_bits(int32_t n) {
   return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
@@ -871,14 +878,14 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         if (!wait(mt.o_full[x], o_i[x] & 1)) break;
         ++o_i[x];
         fence_after();
-        const float f = vs * (direct ? (l > 0.f ? 1.f / l : 0.f) : 1.f);
+        const float f = vs * (direct && l != 0.f ? 1.f / l : 1.f);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float o[32];
           tmem_ld32(to + c * 32, o);
           tmem_wait(o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = l > 0.f ? o[k] * f : 0.f;
+          for (int k = 0; k < 32; ++k) o[k] = l != 0.f ? o[k] * f : 0.f;   // (a NaN row stays one)
           put(c, o);
         }
         fence_before();
@@ -908,9 +915,9 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         ++ml_i;
         const float m2 = mlv[x ^ 1][0][r], l2 = mlv[x ^ 1][1][r];
         const float mm = fmaxf(mref, m2);
-        float w0 = l > 0.f ? dev::exp2_approx(mref - mm) : 0.f, w1 = l2 > 0.f ? dev::exp2_approx(m2 - mm) : 0.f;
+        float w0 = stream_weight(mref, l, mm), w1 = stream_weight(m2, l2, mm);
         const float lsum = l * w0 + l2 * w1;
-        const float f = vs * (direct ? (lsum > 0.f ? 1.f / lsum : 0.f) : 1.f);
+        const float f = vs * (direct && lsum != 0.f ? 1.f / lsum : 1.f);
         w0 *= f;
         w1 *= f;
 #pragma unroll
@@ -1083,13 +1090,13 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant
     for (int k = 0; k < D; ++k) o[k] *= corr;
 #pragma unroll
     for (int c = 0; c < kBatch; ++c) {
-      const float wc = lc[c] > 0.f ? dev::exp2_approx(mc[c] - mx) : 0.f;
+      const float wc = stream_weight(mc[c], lc[c], mx);
       l += wc * lc[c];
 #pragma unroll
       for (int k = 0; k < D; ++k) o[k] += wc * vc[c][k];
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
   uint32_t* out = reinterpret_cast<uint32_t*>(
       prm.out + 2 * (((static_cast<int64_t>(prm.row0 + prm.q0[it] + t) * prm.H + h) * G + (r & (G - 1))) * kHeadDim + d0));
   uint32_t res[D / 2];
@@ -1212,7 +1219,7 @@ cudaError_t launch(const PoolView& pool, const AttendMaps& maps, const AttendArg
   int most = 1;
   for (int i = 0; i < n; ++i) most = std::max(most, ceil_div(items.kv_len[i], kTile));
   int chunk = most;
-  constexpr int kMinChunk = 2, kJoin = 5;
+  constexpr int kMinChunk = 2, kJoin = 6;
   const int64_t room = pool.partial_slots * kPartialSlotFloats / (static_cast<int64_t>(prm.part_rows) * kPartFloats * kq);
   const int64_t want = std::min<int64_t>(num_sms, room);
   if (count(most) < want && most >= kMinChunk + kJoin) {

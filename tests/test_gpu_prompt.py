@@ -216,6 +216,25 @@ def test_rows_around_the_call_stay():
     assert (out[:20] == 7).all() and (out[155:] == 7).all()
 
 
+@pytest.mark.parametrize("kv,act", KINDS)
+@pytest.mark.parametrize("lens,new", [([300, 40], [300, 40]), ([9000], [20]), ([2000] * 10, [600] * 10)])
+def test_a_nan_query_gives_a_nan_row_and_no_other(kv, act, lens, new):
+    """Whole, split and paired tiles; an infinite query element gives no finite row either."""
+    s = Setup(lens, H=4, kv=kv, act=act, seed=2)
+    q = s.rand(sum(new), 16, 2.0)
+    clean = q.clone()
+    q[7, 3, 5] = float("nan")
+    q[11, 9, 100] = float("inf")
+    out = torch.zeros_like(q)
+    pa.pa_prefill_attention(s.pool, 0, new, q, out, SCALE, kv_lens=lens, block_tables=s.tables)
+    assert torch.isnan(out[7, 3]).all() and not torch.isfinite(out[11, 9]).any()
+    ref = torch.zeros_like(q)
+    pa.pa_prefill_attention(s.pool, 0, new, clean, ref, SCALE, kv_lens=lens, block_tables=s.tables)
+    s.check(new, clean, ref, SCALE)
+    out[7, 3], out[11, 9] = ref[7, 3], ref[11, 9]
+    s.check(new, clean, out, SCALE)
+
+
 @pytest.mark.parametrize("lens,new", [([130, 5], [130, 5]), ([9000], [20]), ([2000] * 10, [600] * 10)])
 def test_queries_and_output_at_sixteen_byte_addresses(lens, new):
     """q and out need 16-byte alignment, not more (whole, split and paired tiles)."""
