@@ -1219,7 +1219,7 @@ cudaError_t launch(const PoolView& pool, const AttendMaps& maps, const AttendArg
   int most = 1;
   for (int i = 0; i < n; ++i) most = std::max(most, ceil_div(items.kv_len[i], kTile));
   int chunk = most;
-  constexpr int kMinChunk = 2, kJoin = 6;
+  constexpr int kMinChunk = 2, kJoin = 5;
   const int64_t room = pool.partial_slots * kPartialSlotFloats / (static_cast<int64_t>(prm.part_rows) * kPartFloats * kq);
   const int64_t want = std::min<int64_t>(num_sms, room);
   if (count(most) < want && most >= kMinChunk + kJoin) {
