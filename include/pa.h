@@ -5,7 +5,9 @@
  * cache on one NVIDIA B200 (sm_100a), plus the pieces that keep the cache:
  * a host-side block manager (free list, per-sequence block tables,
  * reference counts, copy-on-write of a shared tail block) and the kernel
- * that writes each step's new K/V rows into their cache slots.
+ * that writes each step's new K/V rows into their cache slots.  Around the
+ * decode it builds block tables and slot maps on the GPU and attends whole
+ * prompts and trees of drafted tokens ("prompts and drafted tokens", below).
  *
  * What the operations compute is fixed by three public pages:
  *   [KVC] "KV cache" (AI engineering visualised): The maths, and the
@@ -277,7 +279,8 @@ pa_status pa_noalloc_check_errors(int32_t device, void *stream, uint32_t *bits);
  * caller's (`block_tables`: device int32 [n][max_blocks_per_seq], such as
  * pa_build_tables keeps, with `kv_lens`: host int32 [n]; seqs NULL).  Tables
  * that the caller keeps are unknown to the pool's block manager: a pool whose
- * blocks are handed out that way should not hand out blocks itself. */
+ * blocks are handed out that way should not hand out blocks itself.  The pages
+ * have no counterpart of these calls. */
 
 /* Extend the block tables of n requests from old_lens[i] to new_lens[i] tokens
  * and list the cache slots of the new tokens, on the GPU.  All pointers are
@@ -323,8 +326,11 @@ pa_status pa_append_kv_slots(pa_pool *pool, int32_t layer, int32_t T, const int3
  * tokens of sequence 0, then 1, ... packed, [sum of q_lens][num_q_heads]
  * [head_dim] act_dtype.  Token t of sequence i stands at position
  * p = len - q_lens[i] + t and attends positions 0 .. p; everything else as
- * pa_decode_attention (heads, group 1, 2, 4 or 8, FP8 scales, fp32 softmax and
- * sums; the probabilities enter the second product rounded to act_dtype).
+ * pa_decode_attention (heads, group 1, 2, 4 or 8, FP8 scales).  Scores, softmax
+ * and sums are fp32; the weights enter the second product rounded to act_dtype,
+ * or to fp16 for an FP8 pool, whose codes are exact in fp16 (bf16 queries are then
+ * held as fp16 times a power of two a row).  A few rows over many positions are
+ * computed in parts, joined through the pool's workspace.
  * q_lens[i] may be 0.  A sequence may be named twice.  Results do not depend on
  * where the blocks lie.  Cache rows inside a sequence's length must be finite:
  * a row that a token does not attend has weight 0 for it, and 0 x inf is NaN
