@@ -90,6 +90,7 @@ struct Unit {
   int32_t n0, n1;       // KV tiles of stream 0 / 1 (dual: n0 = all tiles)
   int32_t part;         // partial index of the unit (x kQ + stream)
   int32_t direct;       // bit x: stream x has all its positions here and writes the output
+  int32_t end0, end1;   // 16-position steps that any row attends in the stream's last tile (dual: the last tile)
 };
 
 struct Meta {
@@ -147,10 +148,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t{1} << 46) |
          (static_cast<uint64_t>(kLayoutSW128) << 61);
 }
-// kind::f16, fp32 accumulators, M = N = 128; B K-major or MN-major.
-__host__ __device__ constexpr uint32_t instr_desc(bool bf16, bool b_mn) {
+// kind::f16, fp32 accumulators, M = 128, N; B K-major or MN-major.
+__host__ __device__ constexpr uint32_t instr_desc(bool bf16, bool b_mn, int N) {
   return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) | (uint32_t(b_mn) << 16) |
-         (uint32_t(128 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+         (uint32_t(N >> 3) << 17) | (uint32_t(128 >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
@@ -468,17 +469,20 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         u.tile0 = c * prm.chunk;
         u.part = w * R::kQ;
         u.direct = 0;
-        int32_t nx[2] = {0, 0};
+        int32_t nx[2] = {0, 0}, end[2] = {0, 0};
 #pragma unroll
         for (int x = 0; x < R::kQ; ++x) {
           if (u.t0 + x * tq >= u.m) break;
           const int32_t last = prm.mask ? u.kv_len - 1 : u.past + min(u.t0 + (x + 1) * tq, u.m) - 1;
           const int32_t nt = last / kTile + 1;
           nx[x] = max(0, min(nt - u.tile0, prm.chunk));
+          end[x] = min(8, (last >> 4) + 1 - (u.tile0 + nx[x] - 1) * 8);
           if (nt <= prm.chunk) u.direct |= 1 << x;
         }
         u.n0 = nx[0];
         u.n1 = nx[1];
+        u.end0 = end[0];
+        u.end1 = end[1];
       }
       if (!begun) dev::grid_dep_wait();
       // the next claim is on its way while this unit is copied
@@ -529,7 +533,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     // tensor core may stand still.
     if (dev::elect_one()) {
       constexpr bool kBf = MMA == kBF16;
-      constexpr uint32_t kIdS = instr_desc(kBf, false), kIdO = instr_desc(kBf, true);
+      constexpr uint32_t kIdS = instr_desc(kBf, false, 0), kIdO = instr_desc(kBf, true, 128);
       const uint64_t q_desc = smem_desc(base, 16, 1024), k_desc = smem_desc(base + R::kOffKv, 16, 2 * kGroup),
                      v_desc = smem_desc(base + R::kOffKv, kGroup, 2 * kGroup);
       uint32_t st = 0, ph = 0;                          // ring stage of the next tile, and its phase
@@ -555,17 +559,19 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         }
         return s;
       };
-      auto issue_s = [&](int x, uint32_t s) {
+      // steps: 16-position steps that any row attends; what lies behind them is not computed
+      auto issue_s = [&](int x, uint32_t s, int32_t steps) {
         fence_after();
+        const uint32_t id = kIdS + (static_cast<uint32_t>(steps * 2) << 17);   // N = 16 steps
         const uint64_t qd = q_desc + (PAIR ? x : 0) * (kOperand >> 4), kd = k_desc + s * (kOperand >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           mma_ss(tmem + x * 128, qd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
-                 kd + (((kk >> 2) * kGroup + (kk & 3) * 32) >> 4), kIdS, kk > 0);
+                 kd + (((kk >> 2) * kGroup + (kk & 3) * 32) >> 4), id, kk > 0);
         }
         commit(bar(mt.s_full[x]));
       };
-      auto issue_pv = [&](int x, uint32_t s, int32_t steps, bool acc) {   // steps: 16-token blocks copied
+      auto issue_pv = [&](int x, uint32_t s, int32_t steps, bool acc) {
         fence_after();
         const uint64_t vd = v_desc + s * (kOperand >> 4);
         if (steps >= 8) {
@@ -581,7 +587,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         if (!wait1(mt.sched_full[unit_i & 1], (unit_i >> 1) & 1)) break;
         const Unit& un = mt.unit[unit_i & 1];
         const int32_t seq_row = un.seq_row, n0 = un.n0, n1 = un.n1, n = max(n0, n1);
-        const int32_t blocks = ((un.kv_len + 15) >> 4) - un.tile0 * 8;    // 16-token blocks from the first tile on
+        const int32_t end0 = un.end0, end1 = un.end1;
         const bool clean = needs_clean(un, n);
         arrive(bar(mt.sched_empty[unit_i & 1]));
         ++unit_i;
@@ -598,13 +604,13 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         };
         auto take_k = [&]() { return wait1(mt.kv_full[st], ph) ? advance() : st; };
         if constexpr (PAIR) {
-          const int32_t nx[2] = {n0, n1};
+          const int32_t nx[2] = {n0, n1}, end[2] = {end0, end1};
           const uint32_t k0 = take_k();
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (!ok || nx[x] == 0 || !wait1(kScaleQ ? mt.q_ready[x] : mt.q_full[x], q_i[x] & 1)) continue;
             ++q_i[x];
-            issue_s(x, k0);
+            issue_s(x, k0, nx[x] == 1 ? end[x] : 8);
             if (nx[x] == 1) commit(bar(mt.q_empty[x]));
           }
           if (!ok) break;
@@ -617,11 +623,11 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
               if (j == 0 && !wait1(mt.o_free[x], (o_i[x]++ & 1) ^ 1)) continue;
               if (!wait1(mt.p_full[x], p_i[x] & 1)) continue;
               ++p_i[x];
-              issue_pv(x, v, blocks - j * 8, j > 0);
+              issue_pv(x, v, j == nx[x] - 1 ? end[x] : 8, j > 0);
               if (x == 1 || j >= nx[1]) commit(bar(mt.kv_empty[v]));
               if (j == nx[x] - 1) commit(bar(mt.o_full[x]));
               if (j + 1 < nx[x]) {
-                issue_s(x, k);
+                issue_s(x, k, j + 1 == nx[x] - 1 ? end[x] : 8);
                 if (j + 1 == nx[x] - 1) commit(bar(mt.q_empty[x]));
               }
               if (j + 1 < n && (x == 1 || j >= nx[1])) commit(bar(mt.kv_empty[k]));
@@ -633,7 +639,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
           for (int32_t i = 0; ok && i < min(2, n); ++i) {
             const uint32_t k = take_k();
             if (!ok) break;
-            issue_s(i, k);
+            issue_s(i, k, i == n - 1 ? end0 : 8);
             commit(bar(mt.kv_empty[k]));
             if (i == n - 1) commit(bar(mt.q_empty[0]));
           }
@@ -642,13 +648,13 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
             const int x = i & 1;
             const uint32_t v = take_v(i);
             if (!ok || !wait1(mt.p_full[x], p_i[x]++ & 1)) break;
-            issue_pv(x, v, blocks - i * 8, i > 1);
+            issue_pv(x, v, i == n - 1 ? end0 : 8, i > 1);
             commit(bar(mt.kv_empty[v]));
             if (i >= n - 2) commit(bar(mt.o_full[x]));
             if (i + 2 < n) {
               const uint32_t k = take_k();
               if (!ok) break;
-              issue_s(x, k);
+              issue_s(x, k, i + 2 == n - 1 ? end0 : 8);
               commit(bar(mt.kv_empty[k]));
               if (i + 2 == n - 1) commit(bar(mt.q_empty[0]));
             }
