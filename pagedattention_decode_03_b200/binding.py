@@ -463,17 +463,21 @@ def pa_build_tables(pool: Pool, old_lens, new_lens, free_blocks, free_head, free
     tokens' slots, on the GPU.  All arguments are int32 device tensors: lengths [n],
     free_blocks [F], free_head / free_head_out [1], block_tables [n][max_blocks_per_seq],
     cu_tokens [n + 1], slots [capacity]."""
-    i32 = _device_pool(pool)[1]
-    n, F, cap = _len1(old_lens, "old_lens"), _len1(free_blocks, "free_blocks"), _len1(slots, "slots")
-    st = lib().pa_build_tables(
-        pool.handle, n, _pool_tensor(pool, old_lens, "old_lens", i32, (n,)),
-        _pool_tensor(pool, new_lens, "new_lens", i32, (n,)),
-        _pool_tensor(pool, free_blocks, "free_blocks", i32, (F,)), F,
-        _pool_tensor(pool, free_head, "free_head", i32, (1,)),
-        _pool_tensor(pool, free_head_out, "free_head_out", i32, (1,)),
-        _pool_tensor(pool, block_tables, "block_tables", i32, (n, pool.max_blocks_per_seq)),
-        _pool_tensor(pool, cu_tokens, "cu_tokens", i32, (n + 1,)),
-        _pool_tensor(pool, slots, "slots", i32, (cap,)), cap, _pool_stream(pool, stream))
+    i32, dev = _device_pool(pool)[1], pool.device
+    n, F, cap = old_lens.numel(), free_blocks.numel(), slots.numel()
+    ptrs = []
+    # (one loop and element counts: the checks are most of a small call's time)
+    for t, size, name in ((old_lens, n, "old_lens"), (new_lens, n, "new_lens"), (free_blocks, F, "free_blocks"),
+                          (free_head, 1, "free_head"), (free_head_out, 1, "free_head_out"),
+                          (block_tables, n * pool.max_blocks_per_seq, "block_tables"),
+                          (cu_tokens, n + 1, "cu_tokens"), (slots, cap, "slots")):
+        if t.dtype is not i32 or t.get_device() != dev or not t.is_contiguous() or t.numel() != size:
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {size} elements on cuda:{dev}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+        ptrs.append(t.data_ptr())
+    old, new, free, head, head_out, tables, cu, sl = ptrs
+    st = lib().pa_build_tables(pool.handle, n, old, new, free, F, head, head_out, tables, cu, sl, cap,
+                               _pool_stream(pool, stream))
     if st != PA_OK:
         _check(st, "pa_build_tables")
 

@@ -26,8 +26,6 @@ namespace {
 // finding each one's request by a binary search in the sums.
 // A slot's block is read from the free list when it is fresh, so no CTA waits
 // for the table entries another one writes.
-constexpr int kTablesThreads = 512;
-constexpr int kTablesWarps = kTablesThreads / 32;
 
 struct TablesParams {
   const int32_t* old_lens;
@@ -54,8 +52,9 @@ __device__ __forceinline__ int last_at_or_below(const int32_t* pre, int n, int32
 }
 
 // SPT: consecutive slots of a thread, which share a search and mostly a block.
-template <int SPT>
+template <int SPT, int kTablesThreads>
 __global__ void __launch_bounds__(kTablesThreads) build_tables_kernel(const __grid_constant__ TablesParams prm) {
+  constexpr int kTablesWarps = kTablesThreads / 32;
   extern __shared__ int32_t sm[];
   int32_t* tok = sm;                  // [n + 1] tokens before request i
   int32_t* blk = sm + prm.n + 1;      // [n + 1] fresh blocks before request i
@@ -176,7 +175,8 @@ __global__ void __launch_bounds__(kTablesThreads) build_tables_kernel(const __gr
     }
   }
   if (!failed)
-    for (int64_t e = gid; e < blk[prm.n]; e += gsize) {
+    // (from the last thread on: in a small call others than those that list slots)
+    for (int64_t e = gsize - 1 - gid; e < blk[prm.n]; e += gsize) {
       const int i = last_at_or_below(blk, prm.n, static_cast<int32_t>(e));
       const int32_t have = (old[i] + B - 1) >> prm.bshift;
       prm.tables[static_cast<int64_t>(i) * prm.mbps + have + (e - blk[i])] = prm.free_blocks[head + e];
@@ -288,19 +288,21 @@ cudaError_t launch_build_tables(const PoolView& pool, int n, const int32_t* old_
   prm.num_blocks = pool.num_blocks;
   prm.cap = cap;
   const size_t smem = (static_cast<size_t>(n) * 3 + 2) * sizeof(int32_t);
-  // Few slots: 4 a thread, for the shortest way through one CTA's.  Many: 16, one
-  // block's worth, so that a search and a block id serve them all: 509 prompts with
-  // 1 M slots 7.9 us; 4 a thread on two or four CTAs an SM took 8.4 and 10.9 us.
-  const bool many = cap > num_sms * kTablesThreads * 4;
-  auto* kernel = many ? build_tables_kernel<16> : build_tables_kernel<4>;
+  // Few slots: 4 a thread, for the shortest way through one CTA's, of 128 threads
+  // where they are enough.  Many: 16, one block's worth, so that a search and a block
+  // id serve them all: 509 prompts with 1 M slots 7.9 us; 4 a thread on two or four
+  // CTAs an SM took 8.4 and 10.9 us.
+  const bool many = cap > num_sms * 512 * 4, few = n <= 128 && cap <= 512;
+  auto* kernel = many ? build_tables_kernel<16, 512> : few ? build_tables_kernel<4, 128> : build_tables_kernel<4, 512>;
+  const int threads = few ? 128 : 512;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>((kTablesMaxSeqs * 3 + 2) * sizeof(int32_t)));
     if (e != cudaSuccess) return e;
   }
-  const int64_t per = kTablesThreads * (many ? 16 : 4);
+  const int64_t per = static_cast<int64_t>(threads) * (many ? 16 : 4);
   const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms, (cap + per - 1) / per)));
-  return launch_pdl(kernel, dim3(grid), dim3(kTablesThreads), smem, stream, prm);
+  return launch_pdl(kernel, dim3(grid), dim3(threads), smem, stream, prm);
 }
 
 cudaError_t launch_append_slots(const PoolView& pool, int layer, int T, const int32_t* slots, const void* k_new,
