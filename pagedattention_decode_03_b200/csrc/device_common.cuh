@@ -247,12 +247,11 @@ __device__ __forceinline__ void grid_dep_launch() {
 
 }  // namespace dev
 
-// Launch `kernel` allowing it to overlap the tail of the previous kernel on
-// `stream` (see grid_dep_wait); on the legacy default stream it is an
-// ordinary launch.
+// Launch `kernel`, with `overlap` allowing it to overlap the tail of the previous
+// kernel on `stream` (see grid_dep_wait).
 template <class... KArgs, class... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t stream, Args&&... args) {
+cudaError_t launch_with(bool overlap, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                        cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -262,8 +261,26 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = stream == nullptr ? 0 : 1;
+  cfg.numAttrs = overlap ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Overlapping, but on the legacy default stream an ordinary launch.
+template <class... KArgs, class... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                       cudaStream_t stream, Args&&... args) {
+  return launch_with(stream != nullptr, kernel, grid, block, smem, stream, std::forward<Args>(args)...);
+}
+
+// Overlapping on every stream.  On the legacy default stream too, the kernel waits
+// for the one before it (grid_dep_wait), and the driver orders it after the work of
+// other blocking streams; prompts of the worked example 16.5 -> 13.8 us a call there,
+// a tree of eight drafts 14.4 -> 10.9 us.  (Such a launch takes the host ~2 us more:
+// for a kernel of 2 us, 5.6 -> 7.5 us a call.)
+template <class... KArgs, class... Args>
+cudaError_t launch_overlapped(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t stream, Args&&... args) {
+  return launch_with(true, kernel, grid, block, smem, stream, std::forward<Args>(args)...);
 }
 
 }  // namespace pa

@@ -1150,7 +1150,7 @@ cudaError_t run(const Params<CAP>& prm, const AttendMaps& maps, const CUtensorMa
     if (attr.numRegs < R::kRegsLaunch) return cudaErrorInvalidConfiguration;
     if (dev < 64) configured |= uint64_t{1} << dev;
   }
-  return launch_pdl(attend_kernel<KV, ACT, PAIR, CAP>, dim3(std::min(num_sms, prm.units)), dim3(R::kThreads), smem, stream,
+  return launch_overlapped(attend_kernel<KV, ACT, PAIR, CAP>, dim3(std::min(num_sms, prm.units)), dim3(R::kThreads), smem, stream,
                     prm, maps.k, maps.v, tmq);
 }
 
@@ -1279,12 +1279,12 @@ cudaError_t launch(const PoolView& pool, const AttendMaps& maps, const AttendArg
     const bool bf = pool.act_dtype == kBF16;
     if (tiles < 32) {
       const dim3 grid(static_cast<unsigned>(tiles * 8));
-      e = bf ? launch_pdl(attend_merge_kernel<kBF16, 8, CAP>, grid, dim3(256), 0, stream, prm, kq)
-             : launch_pdl(attend_merge_kernel<kFP16, 8, CAP>, grid, dim3(256), 0, stream, prm, kq);
+      e = bf ? launch_overlapped(attend_merge_kernel<kBF16, 8, CAP>, grid, dim3(256), 0, stream, prm, kq)
+             : launch_overlapped(attend_merge_kernel<kFP16, 8, CAP>, grid, dim3(256), 0, stream, prm, kq);
     } else {
       const dim3 grid(static_cast<unsigned>(tiles * 4));
-      e = bf ? launch_pdl(attend_merge_kernel<kBF16, 16, CAP>, grid, dim3(256), 0, stream, prm, kq)
-             : launch_pdl(attend_merge_kernel<kFP16, 16, CAP>, grid, dim3(256), 0, stream, prm, kq);
+      e = bf ? launch_overlapped(attend_merge_kernel<kBF16, 16, CAP>, grid, dim3(256), 0, stream, prm, kq)
+             : launch_overlapped(attend_merge_kernel<kFP16, 16, CAP>, grid, dim3(256), 0, stream, prm, kq);
     }
     if (e != cudaSuccess) return e;
     ++*launches;

@@ -284,6 +284,44 @@ def test_other_stream_and_graph_replay():
     assert pa.pa_check_device_errors(s.pool) == 0
 
 
+def test_chained_calls_on_the_default_stream():
+    """Launches may begin while the kernel before them runs: rows that one call writes
+    and the next reads, with torch kernels between and around them, 40 times over."""
+    H, G, n, B = 2, 8, 3, 16
+    s = Setup([], H=H, mbps=20, num_blocks=60, seed=3)
+    dev = dict(dtype=torch.int32, device="cuda")
+    free = torch.randperm(60, generator=torch.Generator().manual_seed(4)).to(torch.int32).cuda()
+    head, old, lens = torch.zeros(1, **dev), [0] * n, [260, 7, 33]
+    cu, slots = torch.zeros(n + 1, **dev), torch.zeros(300, **dev)
+    s.tables, s.lens = torch.zeros((n, 20), **dev), lens
+    a, b = torch.tensor(old, **dev), torch.tensor(lens, **dev)
+    drafts = [17, 7, 20]
+    mask = random_tree_mask(drafts, torch.Generator().manual_seed(2))
+    k, v, q = s.rand(300, H), s.rand(300, H), s.rand(300, H * G, 2.0)
+    qt = q[:sum(drafts)].contiguous()
+    results = []
+    for i in range(40):
+        s.tables.fill_(-1)
+        head.zero_()
+        slots.fill_(-1)
+        for c in s.cache:
+            c.view(torch.uint8).fill_(0xFF)
+        out, outt = torch.full_like(q, float("nan")), torch.full_like(qt, float("nan"))
+        pa.pa_build_tables(s.pool, a, b, free, head, head, s.tables, cu, slots)
+        pa.pa_append_kv_slots(s.pool, 0, slots, k, v)
+        pa.pa_prefill_attention(s.pool, 0, lens, q, out, SCALE, kv_lens=lens, block_tables=s.tables)
+        pa.pa_tree_attention(s.pool, 0, drafts, mask, qt, outt, SCALE, kv_lens=lens, block_tables=s.tables)
+        results.append((out, outt))
+        qn = qt * 1.0                                     # a torch kernel right behind
+        qt, _ = qn, results
+    torch.cuda.synchronize()
+    s.check(lens, q, results[0][0], SCALE)
+    s.check(drafts, qt, results[0][1], SCALE, mask=mask)
+    for out, outt in results[1:]:
+        assert torch.equal(out, results[0][0]) and torch.equal(outt, results[0][1])
+    assert pa.pa_check_device_errors(s.pool) == 0
+
+
 def test_a_corrupt_table_entry_is_reported():
     for bad in (-1, 10 ** 6):
         s = Setup([300, 40], H=1, seed=5)
