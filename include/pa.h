@@ -30,8 +30,9 @@
  *     metadata is updated in stream order: calls on one pool that use
  *     different streams must be ordered by the caller.
  *   - Kernels are launched with programmatic stream serialization (except
- *     on the legacy default stream, where only pa_prefill_attention and
- *     pa_tree_attention are): a launch may start its prologue while
+ *     on the legacy default stream, where only pa_prefill_attention,
+ *     pa_tree_attention and large pa_append_kv_slots and pa_build_tables
+ *     calls are): a launch may start its prologue while
  *     the previous kernel on the stream finishes, and waits for that kernel
  *     before it reads or writes anything earlier work may touch.  The one
  *     exception is a decode launch's L2 prefetch hints for its first cache
