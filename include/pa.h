@@ -48,8 +48,8 @@
  *   - Log: the environment variable PA_LOG (read once per process) set to 1
  *     writes one "[pa] <status>: <message>" line to stderr for every failing
  *     call; 2 adds one line per state-changing call (pool creation,
- *     allocation, fork, free, swap, append, and each decode with the kernel
- *     and work split it chose).  Unset, 0 or not a number: no output.
+ *     allocation, fork, free, swap, append, tables, and each decode or prompt
+ *     attention with the work it was given and how it was split).  Unset, 0 or not a number: no output.
  *   - Profiling: a library built with PA_NVTX defined (the build's --nvtx
  *     option) opens an NVTX range named after the call around every entry
  *     point; otherwise the ranges compile to nothing.

@@ -4,7 +4,7 @@
 //   0 (unset, empty or not a number)  nothing is written
 //   1  every call that returns an error writes "[pa] error: <message>"
 //   2  also one "[pa] ..." line per state-changing call (allocation, fork,
-//      free, swap, append, decode with its chosen kernel and work split)
+//      free, swap, append, tables, decode and prompt attention with the work split)
 // Lines go to stderr, one fprintf each, so lines of concurrent calls do not
 // interleave inside a line.
 //
