@@ -92,10 +92,10 @@ struct Unit {
   int32_t tok0;         // packed row of the unit's first token
   int32_t t0, m;        // first token within its sequence's query tokens, and their number
   int32_t past, kv_len; // positions before the query tokens; all positions
-  int32_t tile0;        // first KV tile
+  int32_t tile0;        // first KV tile (pair: 0)
   int32_t n0, n1;       // KV tiles of stream 0 / 1 (dual: n0 = all tiles)
-  int32_t part;         // partial index of the unit (x kQ + stream)
-  int32_t direct;       // bit x: stream x has all its positions here and writes the output
+  int32_t part;         // partial index of the unit (dual)
+  int32_t direct;       // the unit has all its positions here and writes the output
   int32_t end0, end1;   // 16-position steps that any row attends in the stream's last tile (dual: the last tile)
 };
 
@@ -473,8 +473,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         u.t0 = (qt - 1 - r / ch) * ut;                               // the longest first
         u.tok0 = prm.row0 + prm.q0[lo] + u.t0;
         u.tile0 = c * prm.chunk;
-        u.part = w * R::kQ;
-        u.direct = 0;
+        u.part = w;
+        u.direct = 1;
         int32_t nx[2] = {0, 0}, end[2] = {0, 0};
 #pragma unroll
         for (int x = 0; x < R::kQ; ++x) {
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
           const int32_t nt = last / kTile + 1;
           nx[x] = max(0, min(nt - u.tile0, prm.chunk));
           end[x] = min(8, (last >> 4) + 1 - (u.tile0 + nx[x] - 1) * 8);
-          if (nt <= prm.chunk) u.direct |= 1 << x;
+          if (nt > prm.chunk) u.direct = 0;
         }
         u.n0 = nx[0];
         u.n1 = nx[1];
@@ -863,8 +863,8 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
                       ((static_cast<int64_t>(tok) * prm.H + u.h) * G + g) * kHeadDim;
       // partial: [130][part_rows], so that a warp's rows lie side by side
       const int64_t pr = prm.part_rows;
-      float* part = prm.partials + static_cast<int64_t>(u.part + (PAIR ? x : 0)) * pr * kPartFloats + r;
-      const bool direct = u.direct >> (PAIR ? x : 0) & 1;
+      float* part = prm.partials + u.part * pr * kPartFloats + r;
+      const bool direct = PAIR || u.direct;   // (pairs are taken where no positions are split)
       const bool wide = (reinterpret_cast<uintptr_t>(prm.out) & 31) == 0;  // `out` itself may be 16-byte aligned
       auto put = [&](int c, const float (&o)[32]) {  // columns 32c.. of this row
         if (!row_ok) return;
@@ -890,7 +890,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         if (!wait(mt.o_full[x], o_i[x] & 1)) break;
         ++o_i[x];
         fence_after();
-        const float f = vs * (direct && l != 0.f ? 1.f / l : 1.f);
+        const float f = l != 0.f ? vs / l : 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float o[32];
@@ -903,10 +903,6 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         fence_before();
         __syncwarp();
         if (lane == 0) arrive(bar(mt.o_free[x]));
-        if (!direct && row_ok) {
-          part[kHeadDim * pr] = mref;
-          part[(kHeadDim + 1) * pr] = l;
-        }
       } else {
         // join the two streams; stream x writes d-half x
         bool all = true;
@@ -1052,20 +1048,19 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
 // waits for.  The chunks' O are weighted by 2^(their maximum - the row's) and
 // divided by the sum.  Tiles that had one chunk are done already.
 template <int ACT, int D, int CAP>
-__global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant__ Params<CAP> prm, int kq) {
+__global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant__ Params<CAP> prm) {
   constexpr int kCtas = 64 / D, kBatch = 32 / D;  // CTAs of a query tile; chunks whose loads are under way together
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = 1 << prm.gshift;
-  const int32_t b = blockIdx.x, dq = b % kCtas, x = (b / kCtas) % kq, v = b / kCtas / kq;
-  const int32_t h = v % prm.H, tq = kTile >> prm.gshift, ut = tq * kq;
+  const int32_t b = blockIdx.x, dq = b % kCtas, v = b / kCtas;
+  const int32_t h = v % prm.H, tq = kTile >> prm.gshift;
   int32_t tile = v / prm.H, it = 0, qt = 0;       // the tile's sequence, and its place there (few sequences are split)
   for (; it < prm.n; ++it) {
-    qt = (prm.m[it] + ut - 1) / ut;
+    qt = (prm.m[it] + tq - 1) / tq;
     if (tile < qt) break;
     tile -= qt;
   }
   if (it == prm.n) return;
-  const int32_t m = prm.m[it], past = prm.kv_len[it] - m, t0 = tile * ut + x * tq;
-  if (t0 >= m) return;
+  const int32_t m = prm.m[it], past = prm.kv_len[it] - m, t0 = tile * tq;
   const int32_t last = prm.mask ? prm.kv_len[it] - 1 : past + min(t0 + tq, m) - 1;
   const int32_t nt = last / kTile + 1;
   if (nt <= prm.chunk) return;
@@ -1075,8 +1070,8 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const __grid_constant
   dev::grid_dep_wait();
   dev::grid_dep_launch();
   if (t >= m) return;
-  const int64_t pr = prm.part_rows, step = static_cast<int64_t>(prm.H) * kq * pr * kPartFloats;   // to the next chunk
-  const float* part = prm.partials + (w * kq + x) * pr * kPartFloats + r;
+  const int64_t pr = prm.part_rows, step = prm.H * pr * kPartFloats;   // to the next chunk
+  const float* part = prm.partials + w * pr * kPartFloats + r;
   const int d0 = dq * 2 * D + (warp >> 2) * D;
   float mx = -INFINITY, o[D], l = 0.f;            // the sum so far, against the running maximum
 #pragma unroll
@@ -1197,7 +1192,7 @@ cudaError_t launch(const PoolView& pool, const AttendMaps& maps, const AttendArg
     max_rows = std::max(max_rows, m * G);
   }
   const bool pair = 16 * pairs <= 9 * singles && pairs * H >= num_sms;
-  const int kq = pair ? 2 : 1, ut = tq * kq;
+  const int ut = pair ? 2 * tq : tq;
 
   prm.out = static_cast<uint8_t*>(a.out);
   prm.tables = a.tables;
@@ -1216,7 +1211,7 @@ cudaError_t launch(const PoolView& pool, const AttendMaps& maps, const AttendArg
   prm.bshift = pool.block_size == 32 ? 1 : 0;
   prm.n = n;
   prm.row0 = items.row0;
-  prm.part_rows = pair ? kTile : std::min(kTile, (max_rows + 7) / 8 * 8);
+  prm.part_rows = std::min(kTile, (max_rows + 7) / 8 * 8);
 
   // KV tiles of a chunk: all of a sequence's, unless the units are too few for
   // the SMs; then the smallest chunk that gives each SM one, if that saves more
@@ -1232,9 +1227,9 @@ cudaError_t launch(const PoolView& pool, const AttendMaps& maps, const AttendArg
   for (int i = 0; i < n; ++i) most = std::max(most, ceil_div(items.kv_len[i], kTile));
   int chunk = most;
   constexpr int kMinChunk = 2, kJoin = 5;
-  const int64_t room = pool.partial_slots * kPartialSlotFloats / (static_cast<int64_t>(prm.part_rows) * kPartFloats * kq);
+  const int64_t room = pool.partial_slots * kPartialSlotFloats / (static_cast<int64_t>(prm.part_rows) * kPartFloats);
   const int64_t want = std::min<int64_t>(num_sms, room);
-  if (count(most) < want && most >= kMinChunk + kJoin) {
+  if (!pair && count(most) < want && most >= kMinChunk + kJoin) {
     int lo = kMinChunk, hi = most;                // the smallest chunk with count <= want
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
@@ -1281,16 +1276,16 @@ cudaError_t launch(const PoolView& pool, const AttendMaps& maps, const AttendArg
     // 66 with 16).
     int64_t tiles = 0;
     for (int i = 0; i < n; ++i) tiles += ceil_div(items.q0[i + 1] - items.q0[i], ut);
-    tiles *= H * kq;
+    tiles *= H;
     const bool bf = pool.act_dtype == kBF16;
     if (tiles < 32) {
       const dim3 grid(static_cast<unsigned>(tiles * 8));
-      e = bf ? launch_overlapped(attend_merge_kernel<kBF16, 8, CAP>, grid, dim3(256), 0, stream, prm, kq)
-             : launch_overlapped(attend_merge_kernel<kFP16, 8, CAP>, grid, dim3(256), 0, stream, prm, kq);
+      e = bf ? launch_overlapped(attend_merge_kernel<kBF16, 8, CAP>, grid, dim3(256), 0, stream, prm)
+             : launch_overlapped(attend_merge_kernel<kFP16, 8, CAP>, grid, dim3(256), 0, stream, prm);
     } else {
       const dim3 grid(static_cast<unsigned>(tiles * 4));
-      e = bf ? launch_overlapped(attend_merge_kernel<kBF16, 16, CAP>, grid, dim3(256), 0, stream, prm, kq)
-             : launch_overlapped(attend_merge_kernel<kFP16, 16, CAP>, grid, dim3(256), 0, stream, prm, kq);
+      e = bf ? launch_overlapped(attend_merge_kernel<kBF16, 16, CAP>, grid, dim3(256), 0, stream, prm)
+             : launch_overlapped(attend_merge_kernel<kFP16, 16, CAP>, grid, dim3(256), 0, stream, prm);
     }
     if (e != cudaSuccess) return e;
     ++*launches;

@@ -66,6 +66,78 @@ def test_long_sequences(kv, act, lens, new, G, H):
     assert pa.pa_check_device_errors(s.pool) == 0
 
 
+@pytest.mark.parametrize("kv,act", KINDS)
+@pytest.mark.parametrize("B", [16, 32])
+def test_paired_tiles_of_prompts_and_wide_trees(kv, act, B):
+    """Enough query tiles for two to share each KV tile (a pair for every SM)."""
+    past = [0, 5, 300, 128, 0, 77, 16, 1000] * 5
+    new = [64, 64, 64, 63, 64, 64, 33, 64] * 5
+    s = Setup([p + m for p, m in zip(past, new)], H=4, kv=kv, act=act, B=B, seed=11)
+    mask = random_tree_mask(new, torch.Generator().manual_seed(3))
+    mask[::5] = 0
+    q, out = tree(s, new, mask, 32)
+    s.check(new, q, out, SCALE, mask=mask)
+    lens = [700, 0, 650, 1, 512, 800, 33, 640]
+    s = Setup(lens, H=4, kv=kv, act=act, B=B, seed=12)
+    q, out = prefill(s, lens, 16)
+    s.check(lens, q, out, SCALE)
+    assert pa.pa_check_device_errors(s.pool) == 0
+
+
+def test_decode_and_prompt_attention_on_one_pool():
+    """The single-query decode (stream-K split, fixed partitions) between prompt calls
+    that split positions: they share the pool's workspace and counters."""
+    s = Setup([], H=2, mbps=600, num_blocks=1300)
+    p = pa.pa_pool_create(num_layers=1, num_kv_heads=2, block_size=16, num_blocks=1300, max_seqs=3,
+                          max_blocks_per_seq=600, kv_dtype="bf16", k_cache=s.cache[0], v_cache=s.cache[1])
+    lens = [9000, 700, 33]
+    for i, n in enumerate(lens):
+        pa.pa_alloc_blocks(p, i, n)
+        pa.pa_append_kv(p, 0, [i] * n, list(range(n)), s.rand(n, 2), s.rand(n, 2))
+    s.pool, s.lens = p, lens
+    s.tables = torch.tensor([(pa.pa_get_seq(p, i)[1] + [0] * 600)[:600] for i in range(3)], device="cuda")
+    for part in (0, 512, 0):
+        q, out = prefill(s, [20, 20, 20], 16, seqs=[0, 1, 2])
+        s.check([20, 20, 20], q, out, SCALE)
+        q, dec = s.rand(3, 16, 2.0), torch.empty((3, 16, 128), dtype=torch.bfloat16, device="cuda")
+        one = torch.empty_like(dec)
+        pa.pa_decode_attention(p, 0, [0, 1, 2], q, dec, SCALE, part)
+        pa.pa_prefill_attention(p, 0, [1, 1, 1], q, one, SCALE, seqs=[0, 1, 2])
+        s.check([1, 1, 1], q, dec, SCALE)
+        s.check([1, 1, 1], q, one, SCALE)
+    assert pa.pa_check_device_errors(p) == 0
+
+
+def test_two_pools_on_two_streams():
+    """Calls of different pools may overlap on the GPU, captured ones too."""
+    lens, new = [600, 12000, 64], [600, 16, 64]
+    setups = [Setup(lens, H=2, kv=kv, seed=5) for kv in ("bf16", "fp8_e4m3")]
+    streams = [torch.cuda.Stream() for _ in setups]
+    qs = [s.rand(sum(new), 16, 2.0) for s in setups]
+    outs = [torch.zeros_like(q) for q in qs]
+    torch.cuda.synchronize()
+    graphs = []
+    for s, st, q, out in zip(setups, streams, qs, outs):
+        with torch.cuda.stream(st):
+            pa.pa_prefill_attention(s.pool, 0, new, q, out, SCALE, kv_lens=lens, block_tables=s.tables)
+        st.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for _ in range(3):
+                pa.pa_prefill_attention(s.pool, 0, new, q, out, SCALE, kv_lens=lens, block_tables=s.tables)
+        graphs.append(g)
+        out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, g in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for s, q, out in zip(setups, qs, outs):
+        s.check(new, q, out, SCALE)
+        assert pa.pa_check_device_errors(s.pool) == 0
+
+
 def test_more_sequences_than_one_launch_holds():
     lens = [(i * 37) % 90 for i in range(1100)]
     s = Setup(lens, H=1, seed=3)
