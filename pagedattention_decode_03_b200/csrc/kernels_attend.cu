@@ -21,10 +21,10 @@
 //   dual  both streams serve one query tile and take every other KV tile; their
 //         results are joined in the epilogue (few rows: bound by the KV read).
 // Roles: warp 0 claims work and loads queries, warps 0 and 2 issue the KV tiles'
-// TMA copies, warp 1 issues the MMAs, warp 3 zeroes V rows past a length, warps 4-7 and 8-11 are the two
-// softmax streams (a thread owns a row: its running maximum and sum need no
-// exchange), warps 12-15 convert FP8 codes to fp16 (exact, one instruction a
-// pair; bf16 queries then become fp16 times a power of two a row).
+// TMA copies, warp 1 issues the MMAs, warp 3 zeroes V rows past a length, warps
+// 4-7 and 8-11 are the two softmax streams (a thread owns a row: its running
+// maximum and sum need no exchange), warps 12-15 convert FP8 codes to fp16 (exact,
+// one instruction a pair; bf16 queries then become fp16 times a power of two a row).
 // Work units are claimed from a counter, longest first.  Where there are too
 // few units for the SMs the positions are split into chunks whose partial
 // results (O, maximum, sum) a second kernel joins.
@@ -33,7 +33,7 @@
 // tensor pipe 51% busy: each stream waits for its own S -> softmax -> P V chain);
 // chunks over FP8 caches 0.90 PFLOP/s; trees of 40 to 64 drafts, 32 heads, fp16, 107 us
 // = 5.4 TB/s in a burst, 125 us sustained; eight trees of 20 to 33 drafts over 31,000
-// FP8 tokens 369 us, where the conversion is what a tile waits for.
+// FP8 tokens 370 us, where the conversion is what a tile waits for.
 // Every wait is bounded; one that gives up sets PA_DEVERR_TIMEOUT, and the CTA
 // waits for its copies and MMAs, frees its tensor memory and returns.
 #include <algorithm>
