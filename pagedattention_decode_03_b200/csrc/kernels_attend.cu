@@ -743,7 +743,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         if constexpr (kScaleQ) {
           if (i < (PAIR ? 1 : 2)) {                     // S is made from the converted queries
             sl2 = ldexpf(sl2, mt.q_exp[q_i & 3][PAIR ? x : 0][r]);
-            if (sl2 == 0.f) sl2 = 1e-30f;
+            if (sl2 == 0.f) sl2 = neg ? -1e-30f : 1e-30f;   // (a row of zeros; `none` keeps its sign)
           }
         }
         if (warp_ok) {

@@ -158,6 +158,20 @@ def test_scales(scale, kv):
     s.check(lens, q, out, scale)
 
 
+@pytest.mark.parametrize("scale", [-1e-8, 1e-8, -SCALE])
+@pytest.mark.parametrize("kv,act", KINDS)
+def test_rows_of_zeros_attend_evenly(kv, act, scale):
+    """Padding rows: zero queries weigh all that they attend the same, for scales of
+    both signs and so small that scale x 2^-126 is no number of fp32 any more."""
+    lens, new = [200, 31, 513], [200, 9, 40]
+    s = Setup(lens, H=2, kv=kv, act=act, seed=12)
+    q = s.rand(sum(new), 8)
+    q[::2] = 0
+    out = torch.full_like(q, float("nan"))
+    pa.pa_prefill_attention(s.pool, s.layer, new, q, out, scale, kv_lens=s.lens, block_tables=s.tables)
+    s.check(new, q, out, scale)
+
+
 def test_large_scores_do_not_overflow():
     """Scores of several thousand, rising and falling along the positions."""
     s = Setup([700], H=1, kv="bf16", seed=4)
