@@ -28,7 +28,8 @@
  *     except by pa_check_device_errors.  `stream` is a cudaStream_t passed
  *     as void*; NULL means the legacy default stream.  The pool's device
  *     metadata is updated in stream order: calls on one pool that use
- *     different streams must be ordered by the caller.
+ *     different streams must be ordered by the caller, replays of captured
+ *     calls included.
  *   - Kernels are launched with programmatic stream serialization (except
  *     on the legacy default stream, where only pa_prefill_attention,
  *     pa_tree_attention and large pa_append_kv_slots and pa_build_tables
@@ -281,7 +282,10 @@ pa_status pa_noalloc_check_errors(int32_t device, void *stream, uint32_t *bits);
  * caller's (`block_tables`: device int32 [n][max_blocks_per_seq], such as
  * pa_build_tables keeps, with `kv_lens`: host int32 [n]; seqs NULL).  Tables
  * that the caller keeps are unknown to the pool's block manager: a pool whose
- * blocks are handed out that way should not hand out blocks itself.  The pages
+ * blocks are handed out that way should not hand out blocks itself.  A captured
+ * call on `seqs` carries the table changes that were pending, and each replay
+ * writes them again: capture after an ordinary call on the pool's sequences, when
+ * none are pending, or do not replay once the tables have changed.  The pages
  * have no counterpart of these calls. */
 
 /* Extend the block tables of n requests from old_lens[i] to new_lens[i] tokens

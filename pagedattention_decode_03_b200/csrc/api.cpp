@@ -129,15 +129,37 @@ struct pa_pool {
 
 namespace {
 
+// Zero the error word and the counters, which every kernel leaves zero: on `stream`,
+// or, where that is capturing, at once on a stream of its own (a captured memset would
+// leave them unset for calls before the first replay, and clear the error word at each).
+cudaError_t clear_words(pa_pool* p, cudaStream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(stream, &status);
+  if (e != cudaSuccess) return e;
+  const bool capturing = status != cudaStreamCaptureStatusNone;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaStream_t s = stream;
+  if (capturing) {
+    if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
+    if ((e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking)) != cudaSuccess) s = nullptr;
+  }
+  if (e == cudaSuccess) e = cudaMemsetAsync(p->view.err, 0, sizeof(uint32_t), s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(p->view.counters, 0, counter_bytes(p->d), s);
+  if (capturing) {
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (s) cudaStreamDestroy(s);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+  }
+  return e;
+}
+
 pa_status ensure_device(pa_pool* p, cudaStream_t stream) {
   if (p->host_only) return fail(PA_ERR_INVALID_ARG, "host-only pool: no device buffers");
   if (p->dev_ready) return PA_OK;
   cudaError_t e = cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->d.device);
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-  e = cudaMemsetAsync(p->view.err, 0, sizeof(uint32_t), stream);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(error word)");
-  e = cudaMemsetAsync(p->view.counters, 0, counter_bytes(p->d), stream);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(counters)");
+  e = clear_words(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "clear error word and counters");
 
   const int64_t rows = static_cast<int64_t>(p->d.num_layers) * p->d.num_blocks * p->d.num_kv_heads *
                        p->d.block_size;

@@ -370,6 +370,33 @@ def test_other_stream_and_graph_replay():
     assert pa.pa_check_device_errors(s.pool) == 0
 
 
+def test_a_pools_first_call_may_be_captured():
+    """Its counters are set when the call is captured, not at the first replay, and a
+    replay does not clear an error that a call before it found."""
+    lens, new = [600, 9000, 64], [600, 16, 64]
+    s = Setup(lens, H=2, seed=6)
+    s.pool.workspace.fill_(0xFF)
+    q = s.rand(sum(new), 16, 2.0)
+    out, eager = torch.zeros_like(q), torch.zeros_like(q)
+    torch.cuda.synchronize()
+    st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        pa.pa_prefill_attention(s.pool, 0, new, q, out, SCALE, kv_lens=lens, block_tables=s.tables)
+    pa.pa_prefill_attention(s.pool, 0, new, q, eager, SCALE, kv_lens=lens, block_tables=s.tables)
+    torch.cuda.synchronize()
+    s.check(new, q, eager, SCALE)
+    assert pa.pa_check_device_errors(s.pool) == 0
+    bad = s.tables.clone()
+    bad[0, 0] = -1                                        # block 0 is read instead
+    pa.pa_prefill_attention(s.pool, 0, new, q, eager, SCALE, kv_lens=lens, block_tables=bad)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    s.check(new, q, out, SCALE)
+    assert pa.pa_check_device_errors(s.pool) == pa.PA_DEVERR_BAD_BLOCK
+
+
 def test_chained_calls_on_the_default_stream():
     """Launches may begin while the kernel before them runs: rows that one call writes
     and the next reads, with torch kernels between and around them, 40 times over."""
