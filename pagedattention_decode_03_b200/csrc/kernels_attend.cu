@@ -334,8 +334,9 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&mt.tmem);
-  // (each role that touches global memory waits for the kernel before this one
-  // first; the schedule's first unit comes from the parameters alone)
+  // (each role waits for the kernel before this one before its first bounded wait,
+  // so that kernel's time does not count against the limit; the schedule's first
+  // unit comes from the parameters alone)
 
   // A warp's bounded wait, one outcome for all lanes; false ends the role.
   auto wait = [&](uint64_t& b, uint32_t parity) {
@@ -545,6 +546,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
       uint32_t st = 0, ph = 0;                          // ring stage of the next tile, and its phase
       uint32_t q_i[2] = {0, 0}, p_i[2] = {0, 0}, o_i[2] = {0, 0}, clean_i = 0;
       bool ok = true;
+      dev::grid_dep_wait();
       auto wait1 = [&](uint64_t& b, uint32_t parity) {
         const uint32_t a = bar(b);
         for (uint32_t i = 0; i < kWaitLimit; ++i) {
@@ -677,6 +679,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     // ============================================== V rows past the length
     // Their weights are 0, and 0 x NaN is NaN: zeroed where a block is partly filled.
     uint32_t kv_i = 0, clean_i = 0;
+    dev::grid_dep_wait();
     Unit u;
     while (next_unit(u)) {
       const int32_t n = max(u.n0, u.n1);
@@ -953,6 +956,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     // ==================================================== FP8 codes to fp16 tiles
     uint32_t raw_i = 0, q_i[2] = {0, 0};
     const int tid = threadIdx.x - 384;
+    dev::grid_dep_wait();
     Unit u;
     bool ok = true;
     while (ok && next_unit(u)) {
