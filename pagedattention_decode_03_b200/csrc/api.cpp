@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdio>
 #include <optional>
@@ -37,7 +39,7 @@ pa_status cuda_fail(cudaError_t e, const char* what) {
   return PA_ERR_CUDA;
 }
 
-// Workspace layout: [header: error word | 256 B] [block-table mirror + lengths]
+// Workspace layout: [header: error word, 4 B unused, stamp (16 B) | 256 B] [block-table mirror + lengths]
 // [stream-K arrival counters] [split-KV partial slots]
 constexpr size_t kHeaderBytes = 256;
 constexpr size_t kAlign = 256;
@@ -100,6 +102,10 @@ struct pa_pool {
   pa::PoolView view{};
   bool host_only = false;
   bool dev_ready = false;
+  // the workspace's error word and counters (ensure_words)
+  uint64_t stamp[2] = {0, 0};
+  bool words_ready = false, words_captured = false;
+  unsigned long long words_capture_id = 0;
   int num_sms = 0;
   pa::CacheMaps maps{};
   pa::AttendMaps attend_maps{};
@@ -129,47 +135,57 @@ struct pa_pool {
 
 namespace {
 
-// Zero the error word and the counters, which every kernel leaves zero: on `stream`,
-// or, where that is capturing, at once on a stream of its own (a captured memset would
-// leave them unset for calls before the first replay, and clear the error word at each).
-cudaError_t clear_words(pa_pool* p, cudaStream_t stream) {
+// A stamp that no other pool of this process has: workspaces carry it from the moment
+// their error word and counters are set.
+void make_stamp(const pa_pool* p, uint64_t (&stamp)[2]) {
+  static std::atomic<uint64_t> pools{0};
+  const auto mix = [](uint64_t x) {  // (the finaliser of splitmix64, a bijection)
+    x = (x ^ (x >> 30)) * 0xbf58476d1ce4e5b9ull;
+    x = (x ^ (x >> 27)) * 0x94d049bb133111ebull;
+    return x ^ (x >> 31);
+  };
+  const uint64_t now = static_cast<uint64_t>(std::chrono::steady_clock::now().time_since_epoch().count());
+  stamp[0] = mix(pools.fetch_add(1) + 1);
+  stamp[1] = mix(now ^ mix(reinterpret_cast<uintptr_t>(p)));
+}
+
+// Set the error word and the counters, which every kernel leaves zero, before a
+// pool's first kernel, in the order of `stream`.  A captured launch does so at its
+// replays only, so until a call outside a capture has done it, each capture holds a
+// launch of its own; the kernel leaves a workspace alone that carries the pool's
+// stamp already, so replays keep what other calls have found.
+pa_status ensure_words(pa_pool* p, cudaStream_t stream) {
+  if (p->words_ready) return PA_OK;
   cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
-  cudaError_t e = cudaStreamIsCapturing(stream, &status);
-  if (e != cudaSuccess) return e;
+  unsigned long long id = 0;
+  cudaError_t e = cudaStreamGetCaptureInfo(stream, &status, &id);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetCaptureInfo");
   const bool capturing = status != cudaStreamCaptureStatusNone;
-  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-  cudaStream_t s = stream;
-  if (capturing) {
-    if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
-    if ((e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking)) != cudaSuccess) s = nullptr;
-  }
-  if (e == cudaSuccess) e = cudaMemsetAsync(p->view.err, 0, sizeof(uint32_t), s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(p->view.counters, 0, counter_bytes(p->d), s);
-  if (capturing) {
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (s) cudaStreamDestroy(s);
-    cudaThreadExchangeStreamCaptureMode(&mode);
-  }
-  return e;
+  if (capturing && p->words_captured && p->words_capture_id == id) return PA_OK;
+  e = pa::launch_set_words(p->view, p->stamp, static_cast<int>(counter_bytes(p->d) / sizeof(int32_t)), stream);
+  if (e != cudaSuccess) return cuda_fail(e, "set error word and counters");
+  ++p->launches;
+  p->words_captured = capturing;
+  p->words_capture_id = id;
+  p->words_ready = !capturing;
+  return PA_OK;
 }
 
 pa_status ensure_device(pa_pool* p, cudaStream_t stream) {
   if (p->host_only) return fail(PA_ERR_INVALID_ARG, "host-only pool: no device buffers");
-  if (p->dev_ready) return PA_OK;
-  cudaError_t e = cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->d.device);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-  e = clear_words(p, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "clear error word and counters");
-
-  const int64_t rows = static_cast<int64_t>(p->d.num_layers) * p->d.num_blocks * p->d.num_kv_heads *
-                       p->d.block_size;
-  if (const char* why = pa::encode_cache_maps(p->d.k_cache, p->d.v_cache, p->d.kv_dtype, rows, &p->maps))
-    return fail(PA_ERR_CUDA, why);
-  if (const char* why = pa::encode_attend_maps(p->d.k_cache, p->d.v_cache, p->d.kv_dtype, p->d.block_size, rows,
-                                               &p->attend_maps))
-    return fail(PA_ERR_CUDA, why);
-  p->dev_ready = true;
-  return PA_OK;
+  if (!p->dev_ready) {
+    cudaError_t e = cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->d.device);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+    const int64_t rows = static_cast<int64_t>(p->d.num_layers) * p->d.num_blocks * p->d.num_kv_heads *
+                         p->d.block_size;
+    if (const char* why = pa::encode_cache_maps(p->d.k_cache, p->d.v_cache, p->d.kv_dtype, rows, &p->maps))
+      return fail(PA_ERR_CUDA, why);
+    if (const char* why = pa::encode_attend_maps(p->d.k_cache, p->d.v_cache, p->d.kv_dtype, p->d.block_size, rows,
+                                                 &p->attend_maps))
+      return fail(PA_ERR_CUDA, why);
+    p->dev_ready = true;
+  }
+  return ensure_words(p, stream);
 }
 
 // Ship all pending mirror deltas in a launch of their own.
@@ -434,6 +450,8 @@ pa_status pa_pool_create(const pa_pool_desc* d, pa_pool** out) {
   if (!host_only) {
     uint8_t* ws = static_cast<uint8_t*>(d->workspace);
     v.err = reinterpret_cast<uint32_t*>(ws);
+    v.stamp = reinterpret_cast<uint64_t*>(ws + 8);
+    make_stamp(p.get(), p->stamp);
     v.meta = reinterpret_cast<int32_t*>(ws + kHeaderBytes);
     v.tables = v.meta;
     v.lens = v.meta + static_cast<int64_t>(d->max_seqs) * d->max_blocks_per_seq;
@@ -1230,9 +1248,18 @@ pa_status pa_check_device_errors(pa_pool* p, void* stream, uint32_t* bits) {
   }
   cudaError_t e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-  uint32_t v = 0;
-  e = cudaMemcpy(&v, p->view.err, sizeof(v), cudaMemcpyDeviceToHost);
+  struct {
+    uint32_t err, unused;
+    uint64_t stamp[2];
+  } head{};
+  e = cudaMemcpy(&head, p->view.err, sizeof(head), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(e, "read error word");
+  if (!p->words_ready && (head.stamp[0] != p->stamp[0] || head.stamp[1] != p->stamp[1])) {
+    // captured calls only, none replayed yet
+    *bits = 0;
+    return PA_OK;
+  }
+  const uint32_t v = head.err;
   e = cudaMemset(p->view.err, 0, sizeof(v));
   if (e != cudaSuccess) return cuda_fail(e, "clear error word");
   if (v & PA_DEVERR_TIMEOUT) {

@@ -1,4 +1,5 @@
 // Kernels that write the cache and its device metadata:
+//   * set_words    -- a workspace's error word and arrival counters, once a pool;
 //   * meta_apply   -- applies block-table / length deltas to the device mirror;
 //   * cow_copy     -- copy-on-write of whole physical blocks (every layer, K and
 //                     V), "Managing the KV Cache", Block Tables and Sharing;
@@ -7,7 +8,7 @@
 //                     ("KV cache", paging paragraph; "Managing the KV Cache",
 //                     Answer Key item 2), quantising to OCP FP8 E4M3 for an
 //                     FP8 pool ("Managing the KV Cache", Quantized KV).
-// All three are plain 16-byte vectorised copies bound by HBM bandwidth; the
+// The copies are plain 16-byte vectorised ones bound by HBM bandwidth; the
 // mirror deltas of a step ride in the parameters of whichever of them runs
 // first, so a decode step needs no separate metadata transfer.
 #include <algorithm>
@@ -18,6 +19,23 @@
 
 namespace pa {
 namespace {
+
+struct Stamp {
+  uint64_t v[2];
+};
+
+// Zero the error word and n counters of a workspace that does not carry this stamp yet.
+__global__ void set_words_kernel(uint32_t* err, uint64_t* have, Stamp stamp, int32_t* counters, int n) {
+  const bool done = have[0] == stamp.v[0] && have[1] == stamp.v[1];
+  __syncthreads();  // every thread has looked before one writes
+  if (done) return;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
+  if (threadIdx.x == 0) {
+    *err = 0;
+    have[0] = stamp.v[0];
+    have[1] = stamp.v[1];
+  }
+}
 
 template <int CAP>
 struct MetaParams {
@@ -213,6 +231,13 @@ cudaError_t dispatch_append(const PoolView& pool, int layer, const int64_t* slot
 }
 
 }  // namespace
+
+cudaError_t launch_set_words(const PoolView& pool, const uint64_t (&stamp)[2], int num_counters,
+                             cudaStream_t stream) {
+  // (not overlapped: nothing of it may come before earlier work on the workspace ends)
+  return launch_with(false, set_words_kernel, dim3(1), dim3(512), 0, stream, pool.err, pool.stamp,
+                     Stamp{{stamp[0], stamp[1]}}, pool.counters, num_counters);
+}
 
 cudaError_t launch_meta_apply(const PoolView& pool, const int32_t* idx, const int32_t* val, int n,
                               cudaStream_t stream) {

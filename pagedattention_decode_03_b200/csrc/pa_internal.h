@@ -41,6 +41,7 @@ struct PoolView {
   int32_t* tables;      // = meta
   int32_t* lens;        // = meta + max_seqs*mbps
   float* partials;      // [slots][kPartialSlotFloats]
+  uint64_t* stamp;      // [2] the pool's once error word and counters are set (8 bytes behind the error word)
   int32_t* counters;    // [kMaxWorkers] stream-K arrival counters, zero between launches
   uint32_t* err;
   int64_t partial_slots;
@@ -60,6 +61,11 @@ constexpr int kPayloadSmall = 512;
 constexpr int kPayloadLarge = 7168;
 
 // ------------------------------------------------------------ launchers
+// Zero the error word and the counters of a workspace that does not carry `stamp`
+// yet, and stamp it.
+cudaError_t launch_set_words(const PoolView& pool, const uint64_t (&stamp)[2], int num_counters,
+                             cudaStream_t stream);
+
 // Apply `n` deltas (idx[k], val[k]) to pool.meta.
 cudaError_t launch_meta_apply(const PoolView& pool, const int32_t* idx, const int32_t* val,
                               int n, cudaStream_t stream);

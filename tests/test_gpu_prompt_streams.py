@@ -1,4 +1,5 @@
-"""Order of the prompt-side calls on the legacy default stream against blocking streams.
+"""Order of the prompt-side calls: on the legacy default stream against blocking streams,
+and of a pool's first call after what its stream was given before.
 
 A launch that may begin while the kernel before it runs must still come after work that
 other blocking streams were given before it, and that work must come after all of the
@@ -111,3 +112,96 @@ def test_large_tables_and_appends_between_work_of_a_blocking_stream(blocking):
         _, cu_w, slots_w, head_w = want[i % 2]
         assert c.tolist() == cu_w and h.tolist() == [head_w] and sl.tolist() == slots_w, i
         assert float(k) == float(v) == 1.0 + i % 2
+
+
+# ---------------------------------------------------------- a pool's first call
+LENS, NEW = [600, 9000, 64], [600, 16, 64]
+
+
+def queue_fill(s, stream):
+    """~50 ms of work and, behind it, bytes over the whole workspace, on `stream`."""
+    with torch.cuda.stream(stream):
+        for _ in range(5):
+            torch.cuda._sleep(20_000_000)
+        s.pool.workspace.fill_(0xFF)
+
+
+def attend(s, q, out, tables=None):
+    pa.pa_prefill_attention(s.pool, 0, NEW, q, out, SCALE, kv_lens=LENS, block_tables=s.tables if tables is None else tables)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_first_call_comes_after_what_writes_the_workspace(captured):
+    """The workspace may still be written when the call is made (or captured): the call's
+    own setting of it comes behind that."""
+    s, warm = Setup(LENS, H=2, seed=6), Setup(LENS, H=2, seed=6)
+    q = s.rand(sum(NEW), 16, 2.0)
+    out = torch.full_like(q, float("nan"))
+    attend(warm, q, out)                                  # kernels are loaded, which may wait for the device
+    out.fill_(float("nan"))
+    st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    queue_fill(s, st)
+    with torch.cuda.stream(st):
+        if captured:
+            g.capture_begin()
+            attend(s, q, out)
+            attend(s, q, out)
+            g.capture_end()
+            assert not st.query()                         # what was queued before is still running
+            g.replay()
+            g.replay()
+        else:
+            attend(s, q, out)
+            assert not st.query()
+    torch.cuda.synchronize()
+    s.check(NEW, q, out, SCALE)
+    assert pa.pa_check_device_errors(s.pool) == 0
+
+
+def test_captured_calls_only():
+    """No call of the pool is ever made outside a capture: the state is set at the first
+    replay of whichever graph comes first, once; errors collect over replays."""
+    s = Setup(LENS, H=2, seed=7)
+    s.pool.workspace.fill_(0xFF)
+    q = s.rand(sum(NEW), 16, 2.0)
+    bad = s.tables.clone()
+    bad[0, 0] = -1                                        # block 0 is read instead
+    outs = [torch.full_like(q, float("nan")) for _ in range(2)]
+    st, graphs = torch.cuda.Stream(), [torch.cuda.CUDAGraph() for _ in range(2)]
+    torch.cuda.synchronize()
+    for g, out, tab in zip(graphs, outs, (s.tables, bad)):
+        with torch.cuda.graph(g, stream=st):
+            attend(s, q, out, tab)
+            attend(s, q, out, tab)
+    assert pa.pa_check_device_errors(s.pool) == 0         # nothing has run
+    for k in (1, 0, 0):
+        graphs[k].replay()
+    torch.cuda.synchronize()
+    assert pa.pa_check_device_errors(s.pool) == pa.PA_DEVERR_BAD_BLOCK
+    assert pa.pa_check_device_errors(s.pool) == 0
+    s.check(NEW, q, outs[0], SCALE)
+    graphs[0].replay()
+    attend(s, q, outs[1])
+    torch.cuda.synchronize()
+    s.check(NEW, q, outs[1], SCALE)
+    assert pa.pa_check_device_errors(s.pool) == 0
+
+
+def test_one_workspace_of_two_pools_in_turn():
+    """A pool over the buffer of an earlier one sets it anew."""
+    s = Setup(LENS, H=2, seed=8)
+    q = s.rand(sum(NEW), 16, 2.0)
+    out = torch.empty_like(q)
+    bad = s.tables.clone()
+    bad[0, 0] = -1
+    attend(s, q, out, bad)                                # leaves an error behind
+    torch.cuda.synchronize()
+    first = s.pool
+    s.pool = pa.pa_pool_create(num_layers=1, num_kv_heads=2, block_size=16, num_blocks=s.cache[0].shape[1],
+                               max_seqs=len(LENS), max_blocks_per_seq=s.mbps, kv_dtype="bf16", k_cache=s.cache[0],
+                               v_cache=s.cache[1], workspace=first.workspace)
+    attend(s, q, out)
+    torch.cuda.synchronize()
+    s.check(NEW, q, out, SCALE)
+    assert pa.pa_check_device_errors(s.pool) == 0
