@@ -812,6 +812,9 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
               const float sum = weights(std::true_type{});
               done = !__any_sync(0xffffffffu, row_ok && top > mref + kLazy<MMA>);
               if (done) l += sum;
+              // (stores to tensor memory are asynchronous, and not ordered among
+              // themselves: these are over before the same columns are stored again)
+              else tmem_wait_st();
             }
           } else {
             float mc[8];
