@@ -298,7 +298,8 @@ cudaError_t launch_build_tables(const PoolView& pool, int n, const int32_t* old_
   const bool many = cap > num_sms * 512 * 4, few = n <= 128 && cap <= 512;
   auto* kernel = many ? build_tables_kernel<16, 512> : few ? build_tables_kernel<4, 128> : build_tables_kernel<4, 512>;
   const int threads = few ? 128 : 512;
-  if (smem > 48 * 1024) {
+  // (48 KB need no asking for, but the kernel's static arrays, under 1 KB, count as well)
+  if (smem > 47 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>((kTablesMaxSeqs * 3 + 2) * sizeof(int32_t)));
     if (e != cudaSuccess) return e;
