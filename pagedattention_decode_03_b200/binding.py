@@ -536,7 +536,7 @@ def pa_tree_attention(pool: Pool, layer: int, tree_lens, tree_mask, q, out, scal
     `tree_mask` (int64 or uint64 device tensor [sum(tree_lens)]) sets.  Other
     arguments as pa_prefill_attention."""
     n, s, tab, kl, m, hq, qp, op, rows, _keep = _attend_args(pool, tree_lens, q, out, seqs, kv_lens, block_tables)
-    if tree_mask.element_size() != 8 or tree_mask.is_floating_point():
+    if tree_mask.element_size() != 8 or tree_mask.is_floating_point() or tree_mask.is_complex():
         raise ValueError("tree_mask must be an int64 or uint64 tensor")
     mp = _pool_tensor(pool, tree_mask, "tree_mask", tree_mask.dtype, (rows,))
     st = lib().pa_tree_attention(pool.handle, layer, n, s, tab, kl, m, mp, hq, qp, op, scale,
