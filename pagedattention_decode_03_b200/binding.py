@@ -475,6 +475,8 @@ def pa_build_tables(pool: Pool, old_lens, new_lens, free_blocks, free_head, free
             raise ValueError(f"{name} must be a contiguous int32 tensor of {size} elements on cuda:{dev}, got "
                              f"{t.dtype} {tuple(t.shape)} on {t.device}")
         ptrs.append(t.data_ptr())
+    if block_tables.shape != (n, pool.max_blocks_per_seq):  # its rows are the requests'
+        raise ValueError(f"block_tables must have shape {(n, pool.max_blocks_per_seq)}, got {tuple(block_tables.shape)}")
     old, new, free, head, head_out, tables, cu, sl = ptrs
     st = lib().pa_build_tables(pool.handle, n, old, new, free, F, head, head_out, tables, cu, sl, cap,
                                _pool_stream(pool, stream))

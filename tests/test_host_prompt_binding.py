@@ -74,3 +74,24 @@ def test_other_masks_are_refused(library, mask):
     with pytest.raises(ValueError, match="tree_mask must"):
         attend(True, tree_mask=mask)
     assert not library.calls
+
+
+# ---------------------------------------------------------------- build_tables
+def tables(**change):
+    a = dict(old_lens=dev((N,)), new_lens=dev((N,)), free_blocks=dev((9,)), free_head=dev((1,)),
+             free_head_out=dev((1,)), block_tables=dev((N, MBPS)), cu_tokens=dev((N + 1,)), slots=dev((11,)), stream=0)
+    pa.pa_build_tables(pool(), **(a | change))
+
+
+def test_tables_pass(library):
+    tables()
+    tables(block_tables=dev((0, MBPS)), old_lens=dev((0,)), new_lens=dev((0,)), cu_tokens=dev((1,)), slots=dev((0,)))
+    assert [c[0] for c in library.calls] == ["pa_build_tables"] * 2
+
+
+@pytest.mark.parametrize("shape", [(MBPS, N), (N * MBPS,), (1, N, MBPS), (N, MBPS + 1)])
+def test_tables_of_another_shape_are_refused(library, shape):
+    """[max_blocks][n] holds as many entries, and its rows would be read as [n][max_blocks]."""
+    with pytest.raises(ValueError, match="block_tables must"):
+        tables(block_tables=dev(shape))
+    assert not library.calls
