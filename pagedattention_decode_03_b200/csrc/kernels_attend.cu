@@ -1285,15 +1285,16 @@ cudaError_t launch(const PoolView& pool, const AttendMaps& maps, const AttendArg
     for (int i = 0; i < n; ++i) tiles += ceil_div(items.q0[i + 1] - items.q0[i], ut);
     tiles *= H;
     const bool bf = pool.act_dtype == kBF16;
-    if (tiles < 32) {
-      const dim3 grid(static_cast<unsigned>(tiles * 8));
-      e = bf ? launch_overlapped(attend_merge_kernel<kBF16, 8, CAP>, grid, dim3(256), 0, stream, prm)
-             : launch_overlapped(attend_merge_kernel<kFP16, 8, CAP>, grid, dim3(256), 0, stream, prm);
-    } else {
-      const dim3 grid(static_cast<unsigned>(tiles * 4));
-      e = bf ? launch_overlapped(attend_merge_kernel<kBF16, 16, CAP>, grid, dim3(256), 0, stream, prm)
-             : launch_overlapped(attend_merge_kernel<kFP16, 16, CAP>, grid, dim3(256), 0, stream, prm);
-    }
+    auto join = [&](auto d) {
+      constexpr int D = decltype(d)::value;
+      const dim3 grid(static_cast<unsigned>(tiles * (64 / D)));
+      return bf ? launch_overlapped(attend_merge_kernel<kBF16, D, CAP>, grid, dim3(256), 0, stream, prm)
+                : launch_overlapped(attend_merge_kernel<kFP16, D, CAP>, grid, dim3(256), 0, stream, prm);
+    };
+    if constexpr (CAP == kSmallCap)   // (more sequences are more tiles than that)
+      e = tiles < 32 ? join(std::integral_constant<int, 8>{}) : join(std::integral_constant<int, 16>{});
+    else
+      e = join(std::integral_constant<int, 16>{});
     if (e != cudaSuccess) return e;
     ++*launches;
   }
