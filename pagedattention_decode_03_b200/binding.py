@@ -465,19 +465,17 @@ def pa_build_tables(pool: Pool, old_lens, new_lens, free_blocks, free_head, free
     cu_tokens [n + 1], slots [capacity]."""
     i32, dev = _device_pool(pool)[1], pool.device
     n, F, cap = old_lens.numel(), free_blocks.numel(), slots.numel()
+    tables = _pool_tensor(pool, block_tables, "block_tables", i32, (n, pool.max_blocks_per_seq))
     ptrs = []
     # (one loop and element counts: the checks are most of a small call's time)
     for t, size, name in ((old_lens, n, "old_lens"), (new_lens, n, "new_lens"), (free_blocks, F, "free_blocks"),
                           (free_head, 1, "free_head"), (free_head_out, 1, "free_head_out"),
-                          (block_tables, n * pool.max_blocks_per_seq, "block_tables"),
                           (cu_tokens, n + 1, "cu_tokens"), (slots, cap, "slots")):
         if t.dtype is not i32 or t.get_device() != dev or not t.is_contiguous() or t.numel() != size:
             raise ValueError(f"{name} must be a contiguous int32 tensor of {size} elements on cuda:{dev}, got "
                              f"{t.dtype} {tuple(t.shape)} on {t.device}")
         ptrs.append(t.data_ptr())
-    if block_tables.shape != (n, pool.max_blocks_per_seq):  # its rows are the requests'
-        raise ValueError(f"block_tables must have shape {(n, pool.max_blocks_per_seq)}, got {tuple(block_tables.shape)}")
-    old, new, free, head, head_out, tables, cu, sl = ptrs
+    old, new, free, head, head_out, cu, sl = ptrs
     st = lib().pa_build_tables(pool.handle, n, old, new, free, F, head, head_out, tables, cu, sl, cap,
                                _pool_stream(pool, stream))
     if st != PA_OK:
