@@ -135,18 +135,13 @@ struct pa_pool {
 
 namespace {
 
-// A stamp that no other pool of this process has: workspaces carry it from the moment
-// their error word and counters are set.
-void make_stamp(const pa_pool* p, uint64_t (&stamp)[2]) {
+// A stamp that no other pool has: workspaces carry it from the moment their error
+// word and counters are set.  The first half differs among the pools of a process,
+// the second among processes too; bytes that were never stamped are neither.
+void make_stamp(uint64_t (&stamp)[2]) {
   static std::atomic<uint64_t> pools{0};
-  const auto mix = [](uint64_t x) {  // (the finaliser of splitmix64, a bijection)
-    x = (x ^ (x >> 30)) * 0xbf58476d1ce4e5b9ull;
-    x = (x ^ (x >> 27)) * 0x94d049bb133111ebull;
-    return x ^ (x >> 31);
-  };
-  const uint64_t now = static_cast<uint64_t>(std::chrono::steady_clock::now().time_since_epoch().count());
-  stamp[0] = mix(pools.fetch_add(1) + 1);
-  stamp[1] = mix(now ^ mix(reinterpret_cast<uintptr_t>(p)));
+  stamp[0] = 0x70615f776f726473ull + pools.fetch_add(1);  // ("pa_words")
+  stamp[1] = static_cast<uint64_t>(std::chrono::system_clock::now().time_since_epoch().count());
 }
 
 // Set the error word and the counters, which every kernel leaves zero, before a
@@ -451,7 +446,7 @@ pa_status pa_pool_create(const pa_pool_desc* d, pa_pool** out) {
     uint8_t* ws = static_cast<uint8_t*>(d->workspace);
     v.err = reinterpret_cast<uint32_t*>(ws);
     v.stamp = reinterpret_cast<uint64_t*>(ws + 8);
-    make_stamp(p.get(), p->stamp);
+    make_stamp(p->stamp);
     v.meta = reinterpret_cast<int32_t*>(ws + kHeaderBytes);
     v.tables = v.meta;
     v.lens = v.meta + static_cast<int64_t>(d->max_seqs) * d->max_blocks_per_seq;
