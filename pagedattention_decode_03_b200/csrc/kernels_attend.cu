@@ -812,9 +812,6 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
               const float sum = weights(std::true_type{});
               done = !__any_sync(0xffffffffu, row_ok && top > mref + kLazy<MMA>);
               if (done) l += sum;
-              // (stores to tensor memory are asynchronous, and not ordered among
-              // themselves: these are over before the same columns are stored again)
-              else tmem_wait_st();
             }
           } else {
             float mc[8];
@@ -834,6 +831,9 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
             top = sl2 * mc[0];
           }
           if (!done) {
+            // stores to tensor memory are asynchronous, and not ordered among
+            // themselves: weights stored above are over before they are stored again
+            if constexpr (kSpec) tmem_wait_st();
             // the reference moves, and O is scaled to the new one, after the P V of the
             // step before (complete: S came after it)
             const bool move = top > mref + kLazy<MMA> || (mref == -INFINITY && top > -INFINITY);
