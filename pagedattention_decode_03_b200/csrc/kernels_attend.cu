@@ -65,6 +65,10 @@ template <int MMA>
 constexpr float kLazy = MMA == kBF16 ? 8.f : 3.f;
 template <int MMA>
 constexpr float kBias = MMA == kBF16 ? 0.f : 12.f;
+// From here on the rounding of a scaled score takes up what the weights' type has room
+// for (a step of fp32 is 1/8 at 2^20; fp16 weights pass their largest number from scores
+// of 2^24 on, bf16 ones from 2^31): the rest of such a unit is computed apart.
+constexpr float kFar = 1 << 20;
 
 // Ring depths: up to 224 KB of the SM's 227.
 template <bool PAIR, bool FP8>
@@ -155,6 +159,7 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
          (static_cast<uint64_t>(kLayoutSW128) << 61);
 }
 // kind::f16, fp32 accumulators, M = 128, N; B K-major or MN-major.
+constexpr uint32_t kNegateA = 1u << 13;
 __host__ __device__ constexpr uint32_t instr_desc(bool bf16, bool b_mn, int N) {
   return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) | (uint32_t(b_mn) << 16) |
          (uint32_t(N >> 3) << 17) | (uint32_t(128 >> 4) << 24);
@@ -208,6 +213,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 // 16 columns of this thread's lane, waited for.
 __device__ __forceinline__ void tmem_ld16(uint32_t a, float (&v)[16]) {
@@ -540,7 +550,9 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
     // tensor core may stand still.
     if (dev::elect_one()) {
       constexpr bool kBf = MMA == kBF16;
-      constexpr uint32_t kIdS = instr_desc(kBf, false, 0), kIdO = instr_desc(kBf, true, 128);
+      constexpr uint32_t kIdO = instr_desc(kBf, true, 128);
+      // (under a negative scale S is made of -Q, and scaled by its magnitude)
+      const uint32_t id_s = instr_desc(kBf, false, 0) | (prm.sl2 < 0.f ? kNegateA : 0u);
       const uint64_t q_desc = smem_desc(base, 16, 1024), k_desc = smem_desc(base + R::kOffKv, 16, 2 * kGroup),
                      v_desc = smem_desc(base + R::kOffKv, kGroup, 2 * kGroup);
       uint32_t st = 0, ph = 0;                          // ring stage of the next tile, and its phase
@@ -570,7 +582,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
       // steps: 16-position steps that any row attends; what lies behind them is not computed
       auto issue_s = [&](int x, uint32_t s, int32_t steps) {
         fence_after();
-        const uint32_t id = kIdS + (static_cast<uint32_t>(steps * 2) << 17);   // N = 16 steps
+        const uint32_t id = id_s + (static_cast<uint32_t>(steps * 2) << 17);   // N = 16 steps
         const uint64_t qd = q_desc + (PAIR ? x : 0) * (kOperand >> 4), kd = k_desc + s * (kOperand >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
@@ -728,27 +740,31 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
         lim = u.past + tc + 1;
       }
       const int32_t lim_min = __reduce_min_sync(0xffffffffu, lim);
-      float sl2 = prm.sl2, vs = 1.f;
+      float sl2 = fabsf(prm.sl2), vs = 1.f;
       if constexpr (kFp8) {
         sl2 *= prm.k_scale[prm.layer * prm.H + u.h];
         vs = prm.v_scale[prm.layer * prm.H + u.h];
       }
-      const bool neg = sl2 < 0.f;
-      const float none = neg ? INFINITY : -INFINITY;    // a masked score: -inf once scaled
+      const bool neg = kFp8 && sl2 < 0.f;               // (a negative K scale)
       if constexpr (!kScaleQ)
         if (sl2 == 0.f) sl2 = 1e-30f;                   // equal weights; a masked -inf x sl2 stays -inf
       float mref = -INFINITY, l = 0.f;
-      bool ok = true;
-      for (int32_t i = PAIR ? 0 : x; i < n; i += PAIR ? 1 : 2) {
-        if (!(ok = wait(mt.s_full[x], s_i & 1))) break;
+      bool ok = true, far = false;
+      int32_t i = PAIR ? 0 : x;
+      auto next_scores = [&]() {
+        if (!(ok = wait(mt.s_full[x], s_i & 1))) return false;
         ++s_i;
         fence_after();
         if constexpr (kScaleQ) {
           if (i < (PAIR ? 1 : 2)) {                     // S is made from the converted queries
             sl2 = ldexpf(sl2, mt.q_exp[q_i & 3][PAIR ? x : 0][r]);
-            if (sl2 == 0.f) sl2 = neg ? -1e-30f : 1e-30f;   // (a row of zeros; `none` keeps its sign)
+            if (sl2 == 0.f) sl2 = 1e-30f;               // (a row of zeros)
           }
         }
+        return true;
+      };
+      for (; !neg && i < n; i += PAIR ? 1 : 2) {
+        if (!next_scores()) break;
         if (warp_ok) {
           const int32_t p0 = (u.tile0 + i) * kTile;
           const bool masked = p0 + kTile > lim_min;
@@ -766,7 +782,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
               if (prm.mask && k0 < 32)
                 a |= k0 >= 0 ? static_cast<uint32_t>(bits << k0) : (k0 > -64 ? static_cast<uint32_t>(bits >> -k0) : 0u);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) y[c][k] = a >> k & 1 ? y[c][k] : none;
+              for (int k = 0; k < 32; ++k) y[c][k] = a >> k & 1 ? y[c][k] : -INFINITY;
             }
           }
           // Weights of the row against the reference, their sum, and (MAX) the row's
@@ -805,7 +821,7 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
           };
           // A tile whose maximum does not pass the reference by kLazy, as nearly all
           // after a row's first do, is done with the weights it was given at once.
-          const bool known = kSpec && !neg && __all_sync(0xffffffffu, !row_ok || mref > -INFINITY);
+          const bool known = kSpec && __all_sync(0xffffffffu, !row_ok || mref > -INFINITY);
           bool done = false;
           if (known) {
             if constexpr (kSpec) {
@@ -816,18 +832,11 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
           } else {
             float mc[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mc[k] = none;
-            if (neg) {
+            for (int k = 0; k < 8; ++k) mc[k] = -INFINITY;
 #pragma unroll
-              for (int k = 0; k < 128; k += 2) mc[(k >> 1) & 7] = fminf(mc[(k >> 1) & 7], fminf(y[k >> 5][k & 31], y[k >> 5][(k & 31) + 1]));
+            for (int k = 0; k < 128; k += 2) mc[(k >> 1) & 7] = fmaxf(mc[(k >> 1) & 7], fmaxf(y[k >> 5][k & 31], y[k >> 5][(k & 31) + 1]));
 #pragma unroll
-              for (int k = 1; k < 8; ++k) mc[0] = fminf(mc[0], mc[k]);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 128; k += 2) mc[(k >> 1) & 7] = fmaxf(mc[(k >> 1) & 7], fmaxf(y[k >> 5][k & 31], y[k >> 5][(k & 31) + 1]));
-#pragma unroll
-              for (int k = 1; k < 8; ++k) mc[0] = fmaxf(mc[0], mc[k]);
-            }
+            for (int k = 1; k < 8; ++k) mc[0] = fmaxf(mc[0], mc[k]);
             top = sl2 * mc[0];
           }
           if (!done) {
@@ -843,21 +852,93 @@ __global__ void __launch_bounds__(Ring<PAIR, KV == kFP8>::kThreads, 1)
               mref = top;
               l *= corr;
             }
-            const bool first = i < (PAIR ? 1 : 2);
-            if (!first && __any_sync(0xffffffffu, move)) {
+            if (__any_sync(0xffffffffu, move)) {
+              if (i >= (PAIR ? 1 : 2)) {
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                float o[16];
-                tmem_ld16(to + c * 16, o);
+                for (int c = 0; c < 8; ++c) {
+                  float o[16];
+                  tmem_ld16(to + c * 16, o);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] *= corr;
-                tmem_st16(to + c * 16, reinterpret_cast<const uint32_t(&)[16]>(o));
+                  for (int k = 0; k < 16; ++k) o[k] *= corr;
+                  tmem_st16(to + c * 16, reinterpret_cast<const uint32_t(&)[16]>(o));
+                }
+              }
+              if (__any_sync(0xffffffffu, row_ok && fabsf(mref) >= kFar && mref > -INFINITY)) {
+                if constexpr (kSpec) {                  // scores that weights lie over
+#pragma unroll
+                  for (int c = 0; c < 4; ++c)
+                    tmem_st16(ts + c * 16, reinterpret_cast<const uint32_t(&)[16]>(y[c >> 1][(c & 1) * 16]));
+                }
+                tmem_wait_st();
+                far = true;
+                break;
               }
             }
             l += weights(std::false_type{});
           }
           tmem_wait_st();
         }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(bar(mt.p_full[x]));
+      }
+      // This tile and the unit's others where a reference is far: scores are scaled and
+      // rounded before they are taken from it, which is exact, so the largest weighs 1; no
+      // lag, 16 columns at a time from tensor memory.  (A small loop of its own: code in
+      // the one above costs prompts percents even where it does not run.)
+      for (bool here = far; (far || neg) && i < n; i += PAIR ? 1 : 2, here = false) {
+        if (!here && !next_scores()) break;
+        const int32_t p0 = (u.tile0 + i) * kTile;
+        auto scores = [&](int c, float (&z)[16]) {
+          tmem_ld16(ts + c * 16, z);
+          const int32_t k0 = lim - (p0 + c * 16);
+          uint32_t a = low_bits(k0);
+          if (prm.mask && k0 < 32)
+            a |= k0 >= 0 ? static_cast<uint32_t>(bits << k0) : (k0 > -64 ? static_cast<uint32_t>(bits >> -k0) : 0u);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) z[k] = a >> k & 1 ? __fmul_rn(z[k], sl2) : -INFINITY;
+        };
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          float z[16];
+          scores(c, z);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) top = fmaxf(top, z[k]);
+        }
+        const bool move = top > mref;
+        float corr = 1.f;
+        if (move) {
+          corr = mref == -INFINITY ? 0.f : dev::exp2_approx(mref - top);
+          mref = top;
+          l *= corr;
+        }
+        if (i >= (PAIR ? 1 : 2) && __any_sync(0xffffffffu, move)) {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            float o[16];
+            tmem_ld16(to + c * 16, o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] *= corr;
+            tmem_st16(to + c * 16, reinterpret_cast<const uint32_t(&)[16]>(o));
+          }
+        }
+        const float ref = mref == -INFINITY ? 0.f : mref;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {                   // P over columns that have been read
+          float z[16];
+          uint32_t pk[8];
+          scores(c, z);
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            const float e0 = dev::exp2_approx(__fsub_rn(z[k], ref) + kBias<MMA>);
+            const float e1 = dev::exp2_approx(__fsub_rn(z[k + 1], ref) + kBias<MMA>);
+            l += e0 + e1;
+            pk[k >> 1] = pack2<MMA>(e0, e1);
+          }
+          tmem_st8(ts + c * 8, pk);
+        }
+        tmem_wait_st();
         fence_before();
         __syncwarp();
         if (lane == 0) arrive(bar(mt.p_full[x]));
