@@ -303,7 +303,7 @@ pa_status pa_noalloc_check_errors(int32_t device, void *stream, uint32_t *bits);
  *     (old + j) % B; slots from cu_tokens[n] up to slots_cap are -1, so a call
  *     of a fixed size may carry fewer tokens.
  * n <= 8192.  Checked on the device, reported by pa_check_device_errors:
- * old < 0, new < old or new beyond max_blocks_per_seq * B sets
+ * old < 0, new < old or new beyond max_blocks_per_seq * B or 2^31 - 256 sets
  * PA_DEVERR_BAD_LEN and leaves that request as it is (no blocks, no tokens);
  * more ids needed than free_blocks holds from *free_head on
  * (PA_DEVERR_NO_BLOCKS), or more tokens than slots_cap (PA_DEVERR_BAD_LEN):
@@ -338,7 +338,7 @@ pa_status pa_append_kv_slots(pa_pool *pool, int32_t layer, int32_t T, const int3
  * or to fp16 for an FP8 pool, whose codes are exact in fp16 (bf16 queries are then
  * held as fp16 times a power of two a row).  A few rows over many positions are
  * computed in parts, joined through the pool's workspace.
- * q_lens[i] may be 0.  A sequence may be named twice.  Results do not depend on
+ * q_lens[i] may be 0.  Lengths go up to 2^31 - 256.  A sequence may be named twice.  Results do not depend on
  * where the blocks lie.  Cache rows inside a sequence's length must be finite:
  * a row that a token does not attend has weight 0 for it, and 0 x inf is NaN
  * (slots past the length may hold anything).

@@ -1030,7 +1030,8 @@ pa_status attend_call(pa_pool* p, const char* what, bool tree, int32_t layer, in
     return fail(PA_ERR_INVALID_ARG, "block_tables must be 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(mask) & 7) return fail(PA_ERR_INVALID_ARG, "tree_mask must be 8-byte aligned");
   if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale must be finite");
-  const int64_t max_len = static_cast<int64_t>(p->d.max_blocks_per_seq) * p->d.block_size;
+  const int64_t max_len =
+      std::min<int64_t>(static_cast<int64_t>(p->d.max_blocks_per_seq) * p->d.block_size, pa::kMaxLen);
   int64_t total = 0;
   for (int32_t i = 0; i < n; ++i) {
     int64_t len;
@@ -1041,9 +1042,10 @@ pa_status attend_call(pa_pool* p, const char* what, bool tree, int32_t layer, in
       len = p->bm->len(seqs[i]);
     } else {
       len = kv_lens[i];
-      if (len < 0 || len > max_len)
-        return fail(PA_ERR_INVALID_ARG, call + ": a length outside [0, max_blocks_per_seq * block_size]");
     }
+    if (len < 0 || len > max_len)
+      return fail(PA_ERR_INVALID_ARG,
+                  call + ": a length outside [0, max_blocks_per_seq * block_size], or beyond 2^31 - 256");
     if (q_lens[i] < 0 || q_lens[i] > len)
       return fail(PA_ERR_INVALID_ARG, call + ": query tokens must be in [0, cached tokens]");
     if (tree && q_lens[i] > pa::kTreeMax)

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kTablesThreads) build_tables_kernel(const __gr
   // each thread sums its run of consecutive requests, then a scan over threads
   const int per = (prm.n + kTablesThreads - 1) / kTablesThreads;
   const int i0 = min(prm.n, tid * per), i1 = min(prm.n, i0 + per);
-  const int64_t max_len = static_cast<int64_t>(prm.mbps) << prm.bshift;
+  const int64_t max_len = min(static_cast<int64_t>(prm.mbps) << prm.bshift, static_cast<int64_t>(kMaxLen));
   int64_t st = 0, sb = 0;
   for (int i = i0; i < i1; ++i) {
     int32_t a = prm.old_lens[i], b = prm.new_lens[i];

@@ -175,6 +175,9 @@ cudaError_t launch_decode_tc(const PoolView& pool, const CacheMaps& maps, const 
 // ---------------------------------------------- prompts and drafted tokens
 // Block tables and the slot map from device request lengths (kernels_tables.cu).
 constexpr int kTablesMaxSeqs = 8192;
+// Longest sequence of these calls: lengths are rounded up to blocks and to tiles of 128
+// in 32 bits.
+constexpr int32_t kMaxLen = INT32_MAX - 255;
 cudaError_t launch_build_tables(const PoolView& pool, int n, const int32_t* old_lens, const int32_t* new_lens,
                                 const int32_t* free_blocks, int num_free, const int32_t* free_head,
                                 int32_t* free_head_out, int32_t* tables, int32_t* cu, int32_t* slots, int cap,

@@ -213,3 +213,23 @@ def test_large_appends_chained_with_their_tables(kv, act):
         assert torch.equal(k.view(torch.uint8), ref.k_cache.view(torch.uint8))
         assert torch.equal(v.view(torch.uint8), ref.v_cache.view(torch.uint8))
     assert pa.pa_check_device_errors(p) == 0
+
+
+def test_lengths_near_32_bits_leave_their_request_alone():
+    """A length within 255 of 2^31 cannot be rounded up to blocks in 32 bits."""
+    B, mbps = 16, 1 << 27
+    p = pa.pa_pool_create(num_layers=1, num_kv_heads=1, block_size=B, num_blocks=64, max_seqs=1, max_blocks_per_seq=mbps,
+                          min_partition_tokens=1 << 24)
+    tables = torch.full((1, mbps), 7, dtype=torch.int32, device="cuda")
+    free, head, cu, slots = i32(list(range(64))), i32([5]), i32([-9, -9]), i32([-9] * 40)
+    for old, new, ok in ((2 ** 31 - 20, 2 ** 31 - 1, False), (2 ** 31 - 270, 2 ** 31 - 255, False),
+                         (2 ** 31 - 280, 2 ** 31 - 256, True)):
+        pa.pa_build_tables(p, i32([old]), i32([new]), free, head, head, tables, cu, slots)
+        assert pa.pa_check_device_errors(p) == (0 if ok else pa.PA_DEVERR_BAD_LEN)
+        if not ok:
+            assert cu.tolist() == [0, 0] and slots.tolist() == [-1] * 40 and head.tolist() == [5]
+            assert int((tables != 7).sum()) == 0
+    a, b = 2 ** 31 - 280, 2 ** 31 - 256                    # 2^31 - 272 begins a fresh block
+    assert cu.tolist() == [0, b - a] and head.tolist() == [6] and int((tables != 7).sum()) == 1
+    assert int(tables[0, (b - 1) // B]) == 5
+    assert slots.tolist() == [(7 if t < 2 ** 31 - 272 else 5) * B + t % B for t in range(a, b)] + [-1] * 16
