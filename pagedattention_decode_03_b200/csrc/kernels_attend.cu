@@ -29,11 +29,14 @@
 // few units for the SMs the positions are split into chunks whose partial
 // results (O, maximum, sum) a second kernel joins.
 // Measured on one B200 (64 query / 8 KV heads unless named): prompts of 9,001 and
-// 7,003 tokens, bf16, 2.03 ms = 1.05 PFLOP/s under the power limit (1.15 in a burst;
-// tensor pipe 51% busy: each stream waits for its own S -> softmax -> P V chain);
-// chunks over FP8 caches 0.90 PFLOP/s; trees of 40 to 64 drafts, 32 heads, fp16, 107 us
-// = 5.4 TB/s in a burst, 125 us sustained; eight trees of 20 to 33 drafts over 31,000
-// FP8 tokens 370 us, where the conversion is what a tile waits for.
+// 7,003 tokens, bf16, 2.02 ms = 1.06 PFLOP/s under the power limit (1.2 in a burst);
+// chunks over FP8 caches 0.90 PFLOP/s; trees of 40 to 64 drafts, 32 heads, fp16, 104 us
+// = 5.5 TB/s in a burst, 124 us sustained; eight trees of 20 to 33 drafts over 31,000
+// FP8 tokens 355 us, where the conversion is what a tile waits for.  A pair of tiles of
+// the long prompts takes 3,620 cycles, of which the tensor core needs 2,048; a stream
+// waits 1,390 for its S, loads it in 185, makes weights and maximum in 1,650, stores and
+// hands over in 150, and spends 7,900 a unit on the epilogue and the next unit's start,
+// 245 a tile here.
 // Every wait is bounded; one that gives up sets PA_DEVERR_TIMEOUT, and the CTA
 // waits for its copies and MMAs, frees its tensor memory and returns.
 #include <algorithm>
@@ -61,6 +64,10 @@ constexpr int kPartFloats = kHeadDim + 2;       // of one row: O, maximum, sum, 
 // running maximum only when that passes it by kLazy (in log2 units).  bf16 has
 // fp32's range, so any lag will do; fp16 weights stay under 2^(kLazy + kBias) =
 // 2^15, and are normal numbers down to 2^-26 of the reference's.
+// They are rounded once to the operands' type.  A second product with what that leaves
+// out, as the decode makes it for bf16, took bf16 results from 2.1e-3 of their norm to
+// 1.65e-3, where their own rounding alone is 1.64e-3 (fp16: 2.6e-4 to 2.1e-4), and long
+// prompts from 2.02 to 2.91 ms, 47 trees from 44 to 55 us, FP8 trees from 365 to 520 us.
 template <int MMA>
 constexpr float kLazy = MMA == kBF16 ? 8.f : 3.f;
 template <int MMA>
@@ -282,6 +289,9 @@ __device__ __forceinline__ uint32_t low_bits(int32_t n) {
 }
 
 // ------------------------------------------------------------------- kernel
+// Up to this many sequences a launch carries 1.3 KB of parameters instead of 10.  Room
+// for 128 (2.9 KB) took calls of 1 to 48 sequences 0.5 us longer (16: 8.98 to 9.44 us) and
+// saved those of 49 to 128 as much (64: 12.99 to 12.44 us): small calls go first.
 constexpr int kSmallCap = 48;
 
 template <int KV, int ACT, bool PAIR, int CAP>
@@ -1266,11 +1276,13 @@ cudaError_t launch(const PoolView& pool, const AttendMaps& maps, const AttendArg
   const int H = pool.num_kv_heads, G = a.num_q_heads / H;
   const int tq = kTile / G;
   const int n = items.n;
-  // Pairs of query tiles read each KV tile once for 256 rows: taken where few
-  // of them stay half empty and there is one for each SM (else one tile's two
-  // streams, with the positions split, keep more SMs busy: trees of 20 to 33
-  // drafts over 32K FP8 tokens, 80 pairs, 665 us as pairs and 482 us as single
-  // tiles; ragged prompts, 8B class, 882 us as pairs and 1064 us as single tiles).
+  // Pairs of query tiles read (and convert) each KV tile once for 256 rows: taken where
+  // few of them stay half empty and there is one for each SM.  As pairs and as single
+  // tiles, us: ragged prompts of 32 heads 911 and 1,066, long ones 2,020 and 2,272, FP8
+  // chunks 960 and 1,000; 47 trees of 64 drafts 116 and 135, of 5 to 16 drafts 46 and 43;
+  // eight FP8 trees of 20 to 33 drafts, 80 pairs, 543 and 350: one tile's two streams,
+  // with the positions split, keep more SMs busy.  The border is not exact: 128 pairs of
+  // 33 drafts are 534 and 614, 160 pairs of FP8 chunks 311 and 254 (two rounds of pairs).
   int64_t singles = 0, pairs = 0;
   int max_rows = 0;
   for (int i = 0; i < n; ++i) {
@@ -1303,7 +1315,9 @@ cudaError_t launch(const PoolView& pool, const AttendMaps& maps, const AttendArg
 
   // KV tiles of a chunk: all of a sequence's, unless the units are too few for
   // the SMs; then the smallest chunk that gives each SM one, if that saves more
-  // tiles (~1 us each) than joining the chunks costs (a second kernel, ~4 us).
+  // tiles than joining the chunks costs (a second kernel).  Two units of one tree, a tile
+  // 1.0 us (FP8 1.25): 7 tiles 13.8 us whole and 10.9 split (16.7 and 12.4), 40 tiles
+  // 46 and 13.8 (58 and 15.6), 4 tiles 10.8 whole.
   auto count = [&](int chunk) {
     int64_t u = 0;
     for (int i = 0; i < n; ++i)
