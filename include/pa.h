@@ -140,7 +140,8 @@ size_t pa_workspace_size(const pa_pool_desc *desc);
 /* Validate `desc` and create the host state of a pool.  Needs no GPU and
  * launches nothing: the device state is initialised by the first device
  * call, in the order of its stream (a captured one: when it is replayed; replays
- * of other calls leave the state as it is).  Errors: PA_ERR_INVALID_ARG (shape, dtype, alignment, workspace too
+ * of other calls leave the state as it is; until a call is made outside a capture,
+ * each capture holds that launch once).  Errors: PA_ERR_INVALID_ARG (shape, dtype, alignment, workspace too
  * small, free_order not a permutation). */
 pa_status pa_pool_create(const pa_pool_desc *desc, pa_pool **out);
 
