@@ -116,9 +116,9 @@ def test_sequences_of_two_launches(kv, act):
 @pytest.mark.parametrize("sign", [1, -1])
 def test_scores_as_large_as_the_types_allow(kv, act, lens, new, rising, sign):
     """Scores apart by far more than their rounding: each row's weight is all on one position,
-    whose V row it is, exactly.  K rows are whole multiples of a step, alike in every d, so
-    the products and their sums are exact; one code in eight positions is the largest so far
-    (rising) or positions follow in any order."""
+    whose V row it is, or on positions of one score.  K rows are whole multiples of a step, alike
+    in every d, so the products and their sums are exact; they rise along the cache, or stand
+    in any order."""
     s = Setup(lens, H=4, kv=kv, act=act, seed=5)
     big_q, step = {"bf16": (2.0 ** 60, 2.0 ** 40), "fp16": (2.0 ** 15, 2.0 ** 5), "fp8_e4m3": (2.0 ** 15, 2.0)}[kv]
     if kv == "fp8_e4m3" and act == "bf16":
